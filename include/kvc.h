@@ -64,6 +64,7 @@ typedef enum kvc_status {
 #define KVC_DEV_ERR_SEQLENS 2 /* cu_seqlens malformed (not monotone, past the total) or a sequence shorter than w */
 #define KVC_DEV_ERR_TIMEOUT 4 /* an internal pipeline wait hit its bound (a bug): outputs invalid */
 #define KVC_DEV_ERR_ORDER 8   /* kvc_pivot_update: a layer folded in out of order */
+#define KVC_DEV_ERR_PAGES 16  /* paged cache: a page id outside the pool, or a length outside the block table */
 
 /* Scoring geometry shared by the score entry points. */
 typedef struct kvc_score_params {
@@ -351,6 +352,193 @@ kvc_status kvc_decode_attention(const uint16_t* q, int64_t q_stride_h, const uin
 kvc_status kvc_prefill_attention(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t n,
                                  int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
                                  uint16_t* out, float* lse, int32_t* dev_err, void* stream);
+
+/* Workspace bytes for kvc_prefill_attention_varlen (host only). */
+kvc_status kvc_prefill_varlen_workspace_size(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t batch,
+                                             int64_t total_q, int64_t max_seqlen_q, int64_t max_seqlen_k,
+                                             size_t* bytes);
+
+/*
+ * Causal attention of a packed batch of sequences with every query row's
+ * log-sum-exp: kvc_prefill_attention for prompts of different lengths, and
+ * for chunks of prompts  [FastKV (gist.science 2502.01068) 1: during prefill
+ * every layer runs full attention over the prompt; 2.A: the window rows are
+ * the last positions of the prompt].  Sequence b has the queries
+ * [cu_seqlens_q[b], cu_seqlens_q[b+1]) and the keys [cu_seqlens_k[b],
+ * cu_seqlens_k[b+1]); its lq queries are its last lq positions, so with lk
+ * keys query i sees the keys j <= i + lk - lq:
+ *     s_ij     = scale * q[i, h, :] . k[j, g, :],   g = h / G
+ *     lse[i,h] = ln sum_{j <= i + lk - lq} exp(s_ij)
+ *     out[i,h] = sum_{j <= i + lk - lq} exp(s_ij - lse[i,h]) v[j, g, :]
+ * A query that sees no key (lq > lk) has out = 0 and lse = -inf.  Keys and
+ * values a query does not see (later positions, other sequences) do not enter
+ * its row, whatever they hold: infinities and NaN there change nothing.
+ *  q     [total_q][H][d] bf16, element (i, h, c) at q[i*q_stride_n + h*q_stride_h + c]
+ *  k, v  [total_k][Hkv][d] bf16, each with its own token and head strides
+ *        (e.g. views of one fused [n][(H + 2 Hkv) d] projection)
+ *  cu_seqlens_q, cu_seqlens_k  DEVICE int32 [batch+1], from 0, monotone,
+ *        at most total_q / total_k; entries of out and lse past
+ *        cu_seqlens_q[batch] are left as they were
+ *  batch 1..1024
+ *  max_seqlen_q, max_seqlen_k  upper bounds of lq and lk (host values)
+ *  out   [total_q][H][d] bf16 out, contiguous, 16-byte aligned, or NULL
+ *  lse   [total_q][H] fp32 out, contiguous, or NULL
+ *  ws    kvc_prefill_varlen_workspace_size(...) bytes, 256-B aligned; one
+ *        call at a time per workspace; it need not be zeroed
+ *  dev_err  KVC_DEV_ERR_SEQLENS if a sequence's cu_seqlens are malformed or
+ *        it is longer than the bounds (its rows are left as they were),
+ *        KVC_DEV_ERR_TIMEOUT
+ * head_dim in {64, 128}; at most 128 query heads per KV head; q, k, v 16-byte
+ * aligned, strides multiples of 8 elements.  Rounding as in
+ * kvc_prefill_attention: bf16 operands, fp32 accumulation, the probabilities
+ * enter the output contraction as bf16 and are normalised by the sum of those
+ * rounded values; the log-sum-exp sums the fp32 probabilities.  Deterministic.
+ */
+kvc_status kvc_prefill_attention_varlen(const uint16_t* q, int64_t q_stride_n, int64_t q_stride_h, const uint16_t* k,
+                                        int64_t k_stride_n, int64_t k_stride_h, const uint16_t* v, int64_t v_stride_n,
+                                        int64_t v_stride_h, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                        int32_t batch, int64_t total_q, int64_t total_k, int64_t max_seqlen_q,
+                                        int64_t max_seqlen_k, int32_t num_heads, int32_t num_kv_heads,
+                                        int32_t head_dim, float scale, uint16_t* out, float* lse, void* ws,
+                                        size_t ws_bytes, int32_t* dev_err, void* stream);
+
+/* Paged cache -------------------------------------------------------------- */
+
+/*
+ * The compacted caches of a batch of sequences in pages of one pool  [FastKV
+ * 2.B: the retained entries of every KV head are the cache the later decoding
+ * steps read, and decoding adds to it].  Every KV head of a sequence holds
+ * the same number of entries, but which token an entry belongs to may differ
+ * from head to head (per-head retention).  Entry s of sequence b and KV head
+ * g sits in page p = block_table[b*table_stride + s / page_size] at
+ *     k[p*page_stride + (g*page_size + s % page_size)*head_dim + c]
+ * (the same for v), its weight and position at
+ * weights/pos[(p*num_kv_heads + g)*page_size + s % page_size].
+ * All arrays are device memory of the caller; the struct itself is read
+ * during the call only.
+ */
+typedef struct kvc_paged_cache {
+  uint16_t* k;                /* [num_pages][Hkv][page_size][d] bf16, 16-byte aligned */
+  uint16_t* v;                /* as k */
+  float* weights;             /* [num_pages][Hkv][page_size]: accumulated attention; NULL: none kept */
+  int32_t* pos;               /* [num_pages][Hkv][page_size]: token position of the entry; NULL: none kept */
+  const int32_t* block_table; /* [batch][table_stride]: page ids; only the pages of held entries are read */
+  int32_t* seq_lens;          /* [batch]: entries held per KV head */
+  int32_t* next_pos;          /* [batch]: tokens seen so far; NULL exactly when pos is */
+  int64_t page_stride;        /* elements from page to page of k and of v, >= Hkv*page_size*d, a multiple of 8 */
+  int64_t table_stride;       /* >= max_pages */
+  int32_t num_pages;          /* pages in the pool */
+  int32_t page_size;          /* entries per page: 16, 32, 64, 128 or 256 */
+  int32_t max_pages;          /* pages per sequence the table has room for */
+  int32_t batch;              /* 1..1024 */
+  int32_t num_kv_heads;
+  int32_t head_dim;           /* 64 or 128 */
+} kvc_paged_cache;
+
+/* Workspace bytes for kvc_paged_append (host only). */
+kvc_status kvc_paged_append_workspace_size(const kvc_paged_cache* c, size_t* bytes);
+
+/*
+ * Write tokens behind the entries a paged cache holds  [FastKV 2.B: decoupled
+ * KV retention -- the per-head selected entries of a prompt, or every token].
+ * Sequence b brings the packed tokens [cu_seqlens[b], cu_seqlens[b+1]), len_b
+ * of them.  With idx NULL all are kept, entry r being token r; with idx
+ * [B][Hkv][kk] (local positions, as kvc_select_topk_varlen writes them) KV
+ * head g keeps the first min(kk, len_b) of its row.  For every kept entry r:
+ *     slot = seq_lens[b] + r;  k, v of the token are copied bit for bit
+ *     pos[slot]     = next_pos[b] + local position of the token
+ *     weights[slot] = scores[g*total + packed position], or 0 without scores
+ * and then seq_lens[b] += entries kept, next_pos[b] += len_b.
+ *  k, v       [total][Hkv][d] bf16, same strides, multiples of 8 elements, 16-byte aligned
+ *  cu_seqlens DEVICE int32 [batch+1], or NULL: one token per sequence
+ *             (total == batch), a decoding step's
+ *  max_seqlen an upper bound of len_b (host value; 1 with cu_seqlens NULL)
+ *  scores     [Hkv][total] fp32 contiguous or NULL (read when weights are kept)
+ *  ws         kvc_paged_append_workspace_size bytes, 256-B aligned,
+ *             ZERO-FILLED before its first use (every call leaves it so); one
+ *             call at a time per workspace
+ *  dev_err    KVC_DEV_ERR_SEQLENS: malformed cu_seqlens or len_b >
+ *             max_seqlen (nothing of b is appended); KVC_DEV_ERR_PAGES: the
+ *             entries do not fit the block table (nothing of b is appended)
+ *             or a page id is outside the pool (entries in that page are
+ *             dropped); KVC_DEV_ERR_INDEX: an idx entry outside [0, len_b)
+ *             (a zero row is written, at position -1 with weight 0)
+ * The pages written must not be shared by two sequences of the batch.
+ */
+kvc_status kvc_paged_append(const kvc_paged_cache* c, const uint16_t* k, const uint16_t* v, int64_t stride_n,
+                            int64_t stride_h, const int32_t* cu_seqlens, int64_t total, int64_t max_seqlen,
+                            const int32_t* idx, int64_t kk, const float* scores, void* ws, size_t ws_bytes,
+                            int32_t* dev_err, void* stream);
+
+/* Workspace bytes for kvc_paged_decode_attention (host only). */
+kvc_status kvc_paged_decode_workspace_size(const kvc_paged_cache* c, int32_t num_heads, int64_t max_len,
+                                           int32_t accumulate, size_t* bytes);
+
+/*
+ * Attention of one decode query per query head of every sequence over its
+ * paged entries: kvc_decode_attention for a batch of growing caches  [FastKV
+ * 2.B and 1, as there].  With len = seq_lens[b], over the entries j < len of
+ * KV head g = h / G:
+ *     s_j       = scale * q[b, h, :] . k_j
+ *     lse[b, h] = ln sum_j exp(s_j)
+ *     out[b, h] = sum_j exp(s_j - lse[b, h]) v_j
+ * and, with `accumulate`, the attention the step paid to every entry is added
+ * to the entry's weight  [StructKV 2.A: accumulated attention as a token's
+ * centrality]:
+ *     weights[j] += sum_{h in g} exp(s_j - lse[b, h])       (heads in order)
+ * An empty sequence has out = 0 and lse = -inf.  What the pages hold past the
+ * entries is not used, whatever it is (infinities and NaN included).
+ *  q        [B][H][d] bf16, element (b, h, c) at q[b*q_stride_b + h*q_stride_h + c];
+ *           16-byte aligned, strides multiples of 8
+ *  max_len  upper bound of seq_lens (host value), <= max_pages * page_size
+ *  out      [B][H][d] fp32, contiguous, 16-byte aligned
+ *  lse      [B][H] fp32 contiguous, or NULL
+ *  ws       kvc_paged_decode_workspace_size(...) bytes, 256-B aligned,
+ *           ZERO-FILLED before its first use (every call leaves its counters
+ *           so); one call at a time per workspace
+ *  dev_err  KVC_DEV_ERR_PAGES: a page id outside the pool or a length
+ *           outside [0, max_len] (that sequence: out = 0, lse = -inf, weights
+ *           unchanged); KVC_DEV_ERR_TIMEOUT
+ * At most 16 query heads per KV head.  Pages may be shared by sequences
+ * unless `accumulate` is set.  fp32 accumulation from the bf16 values; the
+ * probabilities enter the output contraction as a sum of bf16 terms good to
+ * ~2^-17 or better.  Deterministic.
+ */
+kvc_status kvc_paged_decode_attention(const kvc_paged_cache* c, const uint16_t* q, int64_t q_stride_b,
+                                      int64_t q_stride_h, int32_t num_heads, float scale, int64_t max_len,
+                                      int32_t accumulate, float* out, float* lse, void* ws, size_t ws_bytes,
+                                      int32_t* dev_err, void* stream);
+
+/* Workspace bytes for kvc_paged_evict (host only). */
+kvc_status kvc_paged_evict_workspace_size(const kvc_paged_cache* c, int64_t max_len, int64_t budget, size_t* bytes);
+
+/*
+ * Bring every sequence of a paged cache back to a budget of entries per KV
+ * head by accumulated attention weight  [FastKV 2.A and 2.B: a budget per KV
+ * head, the most recent tokens always kept; StructKV 2.A: accumulated
+ * attention ranks the tokens].  For each sequence with len = seq_lens[b] >
+ * budget and each KV head, the entries are ranked
+ *     first the recent ones, pos >= next_pos[b] - recent,
+ *     then by weight, the largest first (NaN counts as the lowest),
+ *     equal: the lower slot first
+ * and the first `budget` are kept.  Kept entries in slots < budget stay where
+ * they are; the i-th kept entry of the slots >= budget (in slot order) moves
+ * -- k, v, weight and position -- into the i-th slot < budget that was given
+ * up.  Then seq_lens[b] = budget.  Attention does not depend on the order of
+ * the entries, so nothing else has to move; slots >= budget keep what they
+ * held, and sequences of at most `budget` entries are not touched.
+ *  max_len  upper bound of seq_lens (host value), <= max_pages * page_size
+ *  budget   >= 1; recent in [0, budget]
+ *  ws       kvc_paged_evict_workspace_size(...) bytes, 256-B aligned,
+ *           ZERO-FILLED before its first use (every call leaves its counters
+ *           so); one call at a time per workspace
+ *  dev_err  KVC_DEV_ERR_PAGES: a page id outside the pool or a length outside
+ *           [0, max_len] (nothing of that sequence moves, its length stays)
+ * Needs weights, and pos and next_pos when recent > 0; pos moves if kept.
+ * The pages must not be shared by two sequences of the batch.
+ */
+kvc_status kvc_paged_evict(const kvc_paged_cache* c, int64_t max_len, int64_t budget, int64_t recent, void* ws,
+                           size_t ws_bytes, int32_t* dev_err, void* stream);
 
 /* Residual vector quantisation of retained rows --------------------------- */
 

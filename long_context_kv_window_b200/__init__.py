@@ -27,6 +27,7 @@ KVC_DEV_ERR_INDEX = 1
 KVC_DEV_ERR_SEQLENS = 2
 KVC_DEV_ERR_TIMEOUT = 4
 KVC_DEV_ERR_ORDER = 8
+KVC_DEV_ERR_PAGES = 16
 
 
 class KvcError(RuntimeError):
@@ -38,6 +39,16 @@ class KvcError(RuntimeError):
 class ScoreParams(ctypes.Structure):
     _fields_ = [("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class PagedCacheStruct(ctypes.Structure):
+    """kvc_paged_cache of include/kvc.h."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("next_pos", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("table_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -73,6 +84,16 @@ _SIGS = {
     "kvc_decode_workspace_size": ([_I32, _I32, _I32, _I64, _P], _I32),
     "kvc_decode_attention": ([_P, _I64, _P, _P, _I64, _I32, _I32, _I32, ctypes.c_float, _P, _P, _SZ, _P, _P],
                              _I32),
+    "kvc_prefill_varlen_workspace_size": ([_I32, _I32, _I32, _I32, _I64, _I64, _I64, _P], _I32),
+    "kvc_prefill_attention_varlen": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I32, _I64, _I64, _I64,
+                                      _I64, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P, _SZ, _P, _P], _I32),
+    "kvc_paged_append_workspace_size": ([_P, _P], _I32),
+    "kvc_paged_append": ([_P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _SZ, _P, _P], _I32),
+    "kvc_paged_decode_workspace_size": ([_P, _I32, _I64, _I32, _P], _I32),
+    "kvc_paged_decode_attention": ([_P, _P, _I64, _I64, _I32, ctypes.c_float, _I64, _I32, _P, _P, _P, _SZ, _P, _P],
+                                   _I32),
+    "kvc_paged_evict_workspace_size": ([_P, _I64, _I64, _P], _I32),
+    "kvc_paged_evict": ([_P, _I64, _I64, _I64, _P, _SZ, _P, _P], _I32),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -560,6 +581,273 @@ def kvc_prefill_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, sca
     _check(_call(dev, lib().kvc_prefill_attention, _ptr(q), _ptr(k), _ptr(v), n, H, Hkv, d, sc, _ptr(out),
                  _ptr(lse), _ptr(dev_err), _stream(stream, dev)), "kvc_prefill_attention")
     return out, lse
+
+
+def prefill_varlen_workspace_size(H: int, Hkv: int, d: int, batch: int, total_q: int, max_q: int, max_k: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().kvc_prefill_varlen_workspace_size(H, Hkv, d, batch, total_q, max_q, max_k, ctypes.byref(out)),
+           "kvc_prefill_varlen_workspace_size")
+    return int(out.value)
+
+
+def _launch_stream(stream: Optional[torch.cuda.Stream], dev: torch.device) -> torch.cuda.Stream:
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    if s.device != dev:
+        raise ValueError(f"stream is on {s.device}, the tensors on {dev}")
+    return s
+
+
+def _scratch(nbytes: int, dev: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A workspace for one call: allocated under the stream the call runs on,
+    so that the allocator hands its memory on in that stream's order."""
+    if stream is None:
+        return _workspace(nbytes, dev)
+    with torch.cuda.stream(stream):
+        return _workspace(nbytes, dev)
+
+
+def _used_on(stream: Optional[torch.cuda.Stream], *made: Optional[torch.Tensor]) -> None:
+    """Tell the allocator that results made here are written on `stream`."""
+    if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def kvc_prefill_attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                                 cu_seqlens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int,
+                                 scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                                 lse: Optional[torch.Tensor] = None, want_out: bool = True,
+                                 ws: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                                 stream=None) -> Tuple[Optional[torch.Tensor], torch.Tensor]:
+    """Causal attention of packed sequences: q [total_q][H][d], k and v
+    [total_k][Hkv][d] (bf16, any token and head strides that are multiples of
+    8), cu_seqlens_q and cu_seqlens_k int32 [B+1] on the device.  A sequence's
+    queries are its last positions (all of them in a whole prompt; fewer in a
+    chunk of one).  Returns (out bf16 [total_q][H][d] or None when want_out is
+    False and none was passed, lse fp32 [total_q][H]).  Rows past the last
+    sequence are left as they were."""
+    _bf16(q, "q", 3)
+    _bf16(k, "k", 3)
+    _bf16(v, "v", 3)
+    dev = q.device
+    _same_device(dev, k=k, v=v)
+    total_q, H, d = q.shape
+    total_k, Hkv, dk = k.shape
+    if dk != d or v.shape != k.shape:
+        raise ValueError("q [total_q][H][d], k and v [total_k][Hkv][d] must agree")
+    B = cu_seqlens_q.numel() - 1
+    _vector(cu_seqlens_q, "cu_seqlens_q", B + 1, torch.int32, dev)
+    _vector(cu_seqlens_k, "cu_seqlens_k", B + 1, torch.int32, dev)
+    made_out = made_lse = None
+    if out is None and want_out:
+        out = made_out = torch.empty((total_q, H, d), dtype=torch.bfloat16, device=dev)
+    if out is not None:
+        _dense(out, "out", (total_q, H, d), _BF16_BITS, dev)
+    if lse is None:
+        lse = made_lse = torch.empty((total_q, H), dtype=torch.float32, device=dev)
+    _dense(lse, "lse", (total_q, H), torch.float32, dev)
+    _err_word(dev_err, dev)
+    if ws is None:
+        ws = _scratch(prefill_varlen_workspace_size(H, Hkv, d, B, total_q, max_seqlen_q, max_seqlen_k), dev, stream)
+    sc = float(1.0 / math.sqrt(d) if scale is None else scale)
+    _check(_call(dev, lib().kvc_prefill_attention_varlen, _ptr(q), q.stride(0), q.stride(1), _ptr(k), k.stride(0),
+                 k.stride(1), _ptr(v), v.stride(0), v.stride(1), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, total_q,
+                 total_k, int(max_seqlen_q), int(max_seqlen_k), H, Hkv, d, sc, _ptr(out), _ptr(lse), _ptr(ws),
+                 _ws_bytes(ws, dev), _ptr(dev_err), _stream(stream, dev)), "kvc_prefill_attention_varlen")
+    _used_on(stream, made_out, made_lse)
+    return out, lse
+
+
+# --------------------------------------------------------------------------- #
+# paged cache
+# --------------------------------------------------------------------------- #
+class PagedCache:
+    """The caches of a batch of sequences in pages of one pool, as the
+    kvc_paged_* calls take them (layout: kvc_paged_cache in include/kvc.h).
+
+    k, v        bf16 [num_pages][Hkv][page_size][d], dense within a page (any page stride)
+    block_table int32 [B][max_pages], unit column stride
+    seq_lens    int32 [B]: entries held per KV head
+    weights     fp32 [num_pages][Hkv][page_size] or None: accumulated attention
+    pos         int32 [num_pages][Hkv][page_size] or None: the entries' token positions
+    next_pos    int32 [B], with pos: tokens seen so far
+
+    The tensors are checked once, here; their contents may change at any time
+    (the calls read them on the device), the tensors themselves stay.  Each
+    call that is not given a workspace uses one the cache keeps for the stream
+    it runs on; inside a stream capture it makes one for that graph alone, so
+    that graphs of one cache share none.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 weights: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                 next_pos: Optional[torch.Tensor] = None):
+        _bf16(k, "k", 4)
+        _bf16(v, "v", 4)
+        dev = k.device
+        num_pages, Hkv, page, d = k.shape
+        if v.shape != k.shape or v.stride() != k.stride():
+            raise ValueError("k and v must have the same shape and strides")
+        if k.stride()[1:] != (page * d, d, 1) and k.numel():
+            raise ValueError("k and v must be dense within a page, [Hkv][page_size][d]")
+        _same_device(dev, v=v, block_table=block_table, seq_lens=seq_lens)
+        B = seq_lens.numel()
+        if block_table.dim() != 2:
+            raise ValueError(f"block_table must be [B][max_pages], got shape {tuple(block_table.shape)}")
+        _rows(block_table, "block_table", B, 1, torch.int32, dev)
+        _vector(seq_lens, "seq_lens", B, torch.int32, dev)
+        for name, t, dt in (("weights", weights, torch.float32), ("pos", pos, torch.int32)):
+            if t is not None:
+                _dense(t, name, (num_pages, Hkv, page), dt, dev)
+        if (pos is None) != (next_pos is None):
+            raise ValueError("pos and next_pos go together")
+        _vector(next_pos, "next_pos", B, torch.int32, dev)
+        self.k, self.v, self.weights, self.pos = k, v, weights, pos
+        self.block_table, self.seq_lens, self.next_pos = block_table, seq_lens, next_pos
+        self.device, self.batch, self.num_kv_heads, self.head_dim, self.page_size = dev, B, Hkv, d, page
+        self.max_pages = block_table.shape[1]
+        self.capacity = self.max_pages * page  # entries per sequence
+        adr = [0 if t is None else t.data_ptr() for t in (k, v, weights, pos, block_table, seq_lens, next_pos)]
+        self._c = PagedCacheStruct(*adr, k.stride(0), block_table.stride(0), num_pages, page, self.max_pages, B, Hkv, d)
+        self._ref = ctypes.byref(self._c)
+        self._ws, self._need = {}, {}
+
+    @classmethod
+    def allocate(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, batch: int, max_pages: int,
+                 device, weights: bool = True) -> "PagedCache":
+        """An empty cache; the block table (zeros) is the caller's to fill."""
+        shape = (num_pages, num_kv_heads, page_size)
+        i32 = torch.int32
+        return cls(torch.empty(shape + (head_dim,), dtype=torch.bfloat16, device=device),
+                   torch.empty(shape + (head_dim,), dtype=torch.bfloat16, device=device),
+                   torch.zeros((batch, max_pages), dtype=i32, device=device),
+                   torch.zeros(batch, dtype=i32, device=device),
+                   weights=torch.zeros(shape, dtype=torch.float32, device=device) if weights else None,
+                   pos=torch.zeros(shape, dtype=i32, device=device),
+                   next_pos=torch.zeros(batch, dtype=i32, device=device))
+
+    def _workspace(self, call: str, size_args: tuple, stream: torch.cuda.Stream) -> torch.Tensor:
+        """A workspace of `call`, zero-filled once, on the stream that uses it.
+        The counters that have to start at zero come first and depend on the
+        cache alone, so a workspace serves every call that needs no more."""
+        need = self._need.get((call, size_args))
+        if need is None:
+            out = ctypes.c_size_t(0)
+            _check(getattr(lib(), call + "_workspace_size")(self._ref, *size_args, ctypes.byref(out)),
+                   call + "_workspace_size")
+            need = self._need[call, size_args] = max(int(out.value), 1)
+        capturing = torch.cuda.is_current_stream_capturing()
+        ws = None if capturing else self._ws.get((call, stream.cuda_stream))
+        if ws is None or ws.numel() < need:
+            with torch.cuda.stream(stream):
+                ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            if not capturing:
+                self._ws[call, stream.cuda_stream] = ws
+        return ws
+
+    def _max_len(self, max_len: Optional[int]) -> int:
+        return self.capacity if max_len is None else int(max_len)
+
+
+def kvc_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                     max_seqlen: Optional[int] = None, idx: Optional[torch.Tensor] = None,
+                     scores: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                     dev_err: Optional[torch.Tensor] = None, stream=None) -> PagedCache:
+    """Write tokens k, v [total][Hkv][d] behind the cache's entries: one per
+    sequence, or the packed ones of cu_seqlens int32 [B+1] (max_seqlen bounds
+    them); with idx int32 [B][Hkv][kk] (kvc_select_topk_varlen's) only the
+    selected ones of each KV head.  scores fp32 [Hkv][total] are the entries'
+    first weights.  Lengths and positions move on, on the device."""
+    dev = _kv_pair(k, v)
+    if v is None:
+        raise ValueError("v is missing")
+    _same_device(cache.device, k=k)
+    total, Hkv, d = k.shape
+    if Hkv != cache.num_kv_heads or d != cache.head_dim:
+        raise ValueError(f"k and v must be [total][{cache.num_kv_heads}][{cache.head_dim}], got {tuple(k.shape)}")
+    if cu_seqlens is None:
+        if total != cache.batch or idx is not None:
+            raise ValueError("without cu_seqlens every sequence brings one token, and idx is not taken")
+        max_seqlen = 1
+    else:
+        _vector(cu_seqlens, "cu_seqlens", cache.batch + 1, torch.int32, dev)
+        if max_seqlen is None:
+            raise ValueError("cu_seqlens needs max_seqlen")
+    kk = 0
+    if idx is not None:
+        if idx.dim() != 3:
+            raise ValueError(f"idx must be [B][Hkv][kk], got shape {tuple(idx.shape)}")
+        kk = idx.shape[2]
+        _dense(idx, "idx", (cache.batch, Hkv, kk), torch.int32, dev)
+    if scores is not None:
+        _dense(scores, "scores", (Hkv, total), torch.float32, dev)
+    _err_word(dev_err, dev)
+    st = _launch_stream(stream, dev)
+    if ws is None:
+        ws = cache._workspace("kvc_paged_append", (), st)
+    _check(_call(dev, lib().kvc_paged_append, cache._ref, _ptr(k), _ptr(v), k.stride(0), k.stride(1),
+                 _ptr(cu_seqlens), total, int(max_seqlen), _ptr(idx), kk, _ptr(scores), _ptr(ws), _ws_bytes(ws, dev),
+                 _ptr(dev_err), _stream(st, dev)), "kvc_paged_append")
+    return cache
+
+
+def kvc_paged_decode_attention(q: torch.Tensor, cache: PagedCache, scale: Optional[float] = None,
+                               max_len: Optional[int] = None, accumulate: bool = False,
+                               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                               ws: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                               stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One decode query per head of every sequence, q [B][H][d], over the
+    entries the cache holds; returns (out fp32 [B][H][d], lse fp32 [B][H]).
+    max_len bounds the entries per sequence (default: the block table's
+    room).  accumulate adds every entry's attention to the cache's weights."""
+    _bf16(q, "q", 3)
+    dev = q.device
+    _same_device(cache.device, q=q)
+    B, H, d = q.shape
+    if B != cache.batch or d != cache.head_dim:
+        raise ValueError(f"q must be [{cache.batch}][H][{cache.head_dim}], got {tuple(q.shape)}")
+    if accumulate and cache.weights is None:
+        raise ValueError("accumulate needs a cache with weights")
+    made_out = made_lse = None
+    if out is None:
+        out = made_out = torch.empty((B, H, d), dtype=torch.float32, device=dev)
+    _dense(out, "out", (B, H, d), torch.float32, dev)
+    if lse is None:
+        lse = made_lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+    _dense(lse, "lse", (B, H), torch.float32, dev)
+    _err_word(dev_err, dev)
+    max_len = cache._max_len(max_len)
+    st = _launch_stream(stream, dev)
+    if ws is None:
+        ws = cache._workspace("kvc_paged_decode", (H, max_len, int(accumulate)), st)
+    sc = float(1.0 / math.sqrt(d) if scale is None else scale)
+    _check(_call(dev, lib().kvc_paged_decode_attention, cache._ref, _ptr(q), q.stride(0), q.stride(1), H, sc, max_len,
+                 int(accumulate), _ptr(out), _ptr(lse), _ptr(ws), _ws_bytes(ws, dev), _ptr(dev_err),
+                 _stream(st, dev)), "kvc_paged_decode_attention")
+    _used_on(stream, made_out, made_lse)
+    return out, lse
+
+
+def kvc_paged_evict(cache: PagedCache, budget: int, recent: int, max_len: Optional[int] = None,
+                    ws: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                    stream=None) -> PagedCache:
+    """Bring every sequence back to `budget` entries per KV head: the entries
+    of the last `recent` positions and the largest weights are kept, in place
+    (kept entries above the budget move into the slots given up below it)."""
+    dev = cache.device
+    if cache.weights is None:
+        raise ValueError("eviction ranks by the cache's weights: it has none")
+    if recent and cache.pos is None:
+        raise ValueError("keeping recent entries needs a cache with pos and next_pos")
+    _err_word(dev_err, dev)
+    max_len = cache._max_len(max_len)
+    st = _launch_stream(stream, dev)
+    if ws is None:
+        ws = cache._workspace("kvc_paged_evict", (max_len, int(budget)), st)
+    _check(_call(dev, lib().kvc_paged_evict, cache._ref, max_len, int(budget), int(recent), _ptr(ws),
+                 _ws_bytes(ws, dev), _ptr(dev_err), _stream(st, dev)), "kvc_paged_evict")
+    return cache
 
 
 # --------------------------------------------------------------------------- #

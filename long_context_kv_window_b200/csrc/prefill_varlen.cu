@@ -1,0 +1,600 @@
+// prefill_varlen.cu -- causal attention of packed sequences with every row's
+// log-sum-exp, on tcgen05 with the probabilities kept in TMEM.
+//
+// FastKV (gist.science 2502.01068) section 1 (full attention over the prompt
+// at prefill) and 2.A (the window rows' normalisers); FastKV abstract:
+// grouped-query heads.  Query i of a sequence sees the keys j <= i + lk - lq.
+//
+// The rows of an MMA tile are (token, head of the group) pairs: 128 / G
+// tokens times the G query heads of KV head g, so that a chunk of few tokens
+// still fills the tensor core and every K/V tile serves the whole group.  A
+// CTA holds two such tiles (2 * (128 / G) consecutive tokens) and walks the
+// key tiles of 128 up to its last row's limit:
+//   S_i = Q_i . K_t^T    M = 128 rows, N = 128 keys, K = d, fp32 in TMEM;
+//   P_i = 2^(S_i c - m)  one thread per row, c = scale * log2 e, m the row's
+//                        running reference; P_i goes back into TMEM as bf16
+//                        over S_i, the A operand of
+//   O_i += P_i . V_t     M = 128, N = d, K = 128 keys, fp32 in TMEM.
+// The tensor core's shared-memory reads decide this layout: a 128^3 MMA with
+// both operands in shared memory reads 64 KB in the 512 cycles it computes,
+// all that an SM's shared memory delivers, so P in shared memory (written,
+// then read back) would bound the kernel at two thirds of the MMA rate.
+//
+// The reference m moves only when a row's max passes it by more than 8 log2
+// units (p <= 2^8 otherwise); then the warp rescales its rows of O_i in TMEM:
+// S_i(t) was issued after O_i(t-1), so its completion means O_i is at rest.
+//
+// Keys a row does not see are masked before the max.  A masked value row still
+// meets p = 0 in the MMA, and 0 * inf = NaN; so the value tiles in which some
+// row of the block masks a key are looked over first, infinities and NaN in
+// them are set to 0, and the rows that do see such a value add it at the end.
+//
+// Warps: 0 TMA producer, 1 MMA issuer (and TMEM), 2..3 value check, 4..7 and
+// 8..11 the softmax of tiles 0 and 1 (one row per thread).  Every wait is
+// bounded; on a timeout the CTA records KVC_DEV_ERR_TIMEOUT, lets its copies
+// and MMAs land, frees TMEM and exits.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "tc.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int kVT = 128;          // rows per MMA tile, keys per key tile
+constexpr int kVBlock = 384;      // 12 warps
+constexpr int kVMaxClean = 4;     // key tiles of a block in which some row masks a key: at most 3
+constexpr float kVSlack = 8.f;    // log2 units a row max may pass its reference by
+constexpr double kLn2 = 0.6931471805599453;
+constexpr double kLog2e = 1.4426950408889634;
+
+struct VarArgs {
+  const uint16_t* v;     // for the rows that see a non-finite value
+  int64_t v_sn, v_sh;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int64_t total_q, total_k, max_q, max_k;
+  int batch, H, Hkv, G;
+  int nt;                // tokens per tile: 128 / G
+  float c;               // scale * log2(e)
+  uint16_t* out;         // [total_q][H][D] or nullptr
+  float* lse;            // [total_q][H] or nullptr
+  int32_t* err;
+};
+
+template <int D>
+struct VarSmem {
+  static constexpr int kBlk = kVT * 128;         // 128 rows x 128 B: one 64-column block (16 KB)
+  static constexpr int kTile = (D / 64) * kBlk;  // a 128 x D bf16 tile
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kRing = 2 * kTile;        // Q: two tiles, then the K/V ring
+  static constexpr int kBarOff = kRing + kStages * kTile;
+  static constexpr size_t kBytes = 1024 + (size_t)kBarOff + 1024;
+  static_assert(kBytes <= 232448, "shared memory of one CTA");
+};
+
+struct VarBars {
+  uint64_t qfull, full[8], empty[8];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t clean[kVMaxClean];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort, dirty;
+  int seq, blk;  // this CTA's sequence (-1: none) and block of it
+};
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, A bf16 (two K values per 32-bit column).
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// MN-major operand descriptor, 128-byte swizzle: 64 MN-consecutive elements
+// per 128-byte row, K rows at 128 B; `lbo` bytes between 64-element MN
+// blocks, 1024 B between 8-row K groups.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t smem_addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// Blocks of sequence b (0 if it is empty or malformed; *bad then says which).
+__device__ __forceinline__ int seq_blocks(const VarArgs& a, int b, bool* bad) {
+  const int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+  *bad = q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k || q1 - q0 > a.max_q ||
+         k1 - k0 > a.max_k;
+  return *bad ? 0 : (int)((q1 - q0 + 2 * a.nt - 1) / (2 * a.nt));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kVBlock, 1)
+prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap, const VarArgs a) {
+  using L = VarSmem<D>;
+  constexpr int kCB = D / 64;        // 64-column blocks of a tile
+  constexpr uint32_t kO = 256;       // first O column; S at 0 and 128
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  VarBars* bars = reinterpret_cast<VarBars*>(sm + L::kBarOff);
+  static_assert(sizeof(VarBars) <= 1024, "barrier block");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = (int)(blockIdx.x % (unsigned)a.Hkv);  // the heads of a block side by side
+
+  if (tid == 0) {
+    tc::mbar_init(&bars->qfull, 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      tc::mbar_init(&bars->full[s], 1);
+      tc::mbar_init(&bars->empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bars->s_full[i], 1);
+      tc::mbar_init(&bars->p_full[i], 4);
+      tc::mbar_init(&bars->o_done[i], 1);
+    }
+    for (int i = 0; i < kVMaxClean; ++i) tc::mbar_init(&bars->clean[i], 2);
+    tc::mbar_init(&bars->mma_done, 1);
+    bars->abort = 0;
+    bars->dirty = 0;
+    tc::fence_mbar_init();
+    tc::prefetch_tmap(&qmap);
+    tc::prefetch_tmap(&kmap);
+    tc::prefetch_tmap(&vmap);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&bars->tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  // rows past the tokens of a tile (128 % G of them) are zero
+  for (int i = tid; i < 2 * kCB * 8 * (kVT - a.nt * a.G); i += kVBlock) {
+    const int blk = i / (8 * (kVT - a.nt * a.G)), j = i % (8 * (kVT - a.nt * a.G));
+    *reinterpret_cast<uint4*>(sm + blk * L::kBlk + a.nt * a.G * 128 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  tc::fence_proxy_async_smem();
+  pdl_wait();  // the inputs may come from the previous kernel of the stream
+  if (warp == 2) {
+    // the block of this CTA: sequences in order, the last (longest) block of
+    // each first; the first CTA looks at every sequence, for the error word
+    const bool first = blockIdx.x == 0;
+    int left = (int)(blockIdx.x / (unsigned)a.Hkv), found = -1, blk = 0;
+    for (int b0 = 0; b0 < a.batch && (found < 0 || first); b0 += 32) {
+      bool bad = false;
+      const int nb = b0 + lane < a.batch ? seq_blocks(a, b0 + lane, &bad) : 0;
+      if (bad && first) set_dev_err(a.err, KVC_DEV_ERR_SEQLENS);
+      int inc = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, inc > left);
+      if (hit && found < 0) {
+        const int src = __ffs(hit) - 1;
+        const int nbs = __shfl_sync(0xffffffffu, nb, src), before = __shfl_sync(0xffffffffu, inc - nb, src);
+        found = b0 + src;
+        blk = nbs - 1 - (left - before);
+      }
+      left -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      bars->seq = found;
+      bars->blk = blk;
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort_flag = &bars->abort;
+  const int seq = bars->seq;
+  int n_tiles[2] = {0, 0};  // key tiles up to the last row of each MMA tile
+  int t_mask = 0;           // first key tile in which some row of the block masks a key
+  int q0 = 0, k0 = 0, lq = 0, lk = 0, i0 = 0;
+  if (seq >= 0) {
+    q0 = a.cu_q[seq];
+    k0 = a.cu_k[seq];
+    lq = a.cu_q[seq + 1] - q0;
+    lk = a.cu_k[seq + 1] - k0;
+    i0 = bars->blk * 2 * a.nt;
+    for (int i = 0; i < 2; ++i) {
+      const int lim = std::min(lq - i0, (i + 1) * a.nt) - 1 + i0 + lk - lq;  // the tile's last row sees keys up to here
+      n_tiles[i] = i * a.nt < lq - i0 && lim >= 0 ? lim / kVT + 1 : 0;
+    }
+    t_mask = std::max(0, i0 + lk - lq + 1) / kVT;
+  }
+  const int nt = std::max(n_tiles[0], n_tiles[1]);
+  int issued = 0;  // producer: K and V tiles requested
+
+  if (warp == 0) {
+    // ---- producer: Q, then K(0), V(0), K(1), V(1), ...
+    if (lane == 0 && nt > 0) {
+      tc::mbar_arrive_expect_tx(&bars->qfull, (uint32_t)(2 * kCB * a.nt * a.G * 128));
+      for (int i = 0; i < 2; ++i)
+        for (int cb = 0; cb < kCB; ++cb)
+          tc::tma_load_3d(sm + i * L::kTile + cb * L::kBlk, &qmap, &bars->qfull, cb * 64, g * a.G,
+                          q0 + i0 + i * a.nt);
+      for (int j = 0; j < 2 * nt; ++j) {
+        const int s = j % L::kStages;
+        if (j >= L::kStages && !tc::mbar_wait(&bars->empty[s], ((j / L::kStages) - 1) & 1, abort_flag)) break;
+        tc::mbar_arrive_expect_tx(&bars->full[s], (uint32_t)L::kTile);
+        for (int cb = 0; cb < kCB; ++cb)
+          tc::tma_load_3d(sm + L::kRing + s * L::kTile + cb * L::kBlk, (j & 1) ? &vmap : &kmap, &bars->full[s],
+                          cb * 64, g, k0 + (j >> 1) * kVT);
+        issued = j + 1;
+      }
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer: S of key tile 0, then for every key tile and MMA tile
+    // the output and the next logits (which overwrite the P just used: the
+    // tensor core runs them in the order they are issued)
+    if (lane == 0 && nt > 0) {
+      const uint32_t id_s = tc::idesc_bf16_f32(128, 128);
+      const uint32_t id_o = tc::idesc_bf16_f32(128, D) | (1u << 16);  // B (V) MN-major
+      const uint64_t q_desc = tc::desc_k_sw128(tc::smem_u32(sm));
+      const uint64_t k_desc = tc::desc_k_sw128(tc::smem_u32(sm + L::kRing));
+      const uint64_t v_desc = desc_mn(tc::smem_u32(sm + L::kRing), (uint32_t)L::kBlk);
+      auto logits = [&](int i, int t) {
+        const uint64_t qd = q_desc + (uint64_t)((uint32_t)(i * L::kTile) >> 4);
+        const uint64_t kd = k_desc + (uint64_t)((uint32_t)(((2 * t) % L::kStages) * L::kTile) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (uint32_t)((ks >> 2) * L::kBlk + (ks & 3) * 32) >> 4;
+          tc::mma_bf16(tmem + (uint32_t)(128 * i), qd + off, kd + off, id_s, ks != 0);
+        }
+        tc::mma_commit(&bars->s_full[i]);
+      };
+      auto wait_full = [&](int j) { return tc::mbar_wait(&bars->full[j % L::kStages], (j / L::kStages) & 1, abort_flag); };
+      bool ok = tc::mbar_wait(&bars->qfull, 0, abort_flag) && wait_full(0);
+      if (ok) {
+        tc::tc_fence_after();
+        for (int i = 0; i < 2; ++i)
+          if (n_tiles[i] > 0) logits(i, 0);
+        tc::mma_commit(&bars->empty[0]);  // K(0) is read
+      }
+      for (int t = 0; ok && t < nt; ++t) {
+        const int vj = 2 * t + 1, vs = vj % L::kStages;
+        ok = wait_full(vj);
+        if (ok && t >= t_mask) ok = tc::mbar_wait(&bars->clean[t - t_mask], 0, abort_flag);
+        if (ok && t + 1 < nt) ok = wait_full(vj + 1);
+        for (int i = 0; ok && i < 2; ++i) {
+          if (t >= n_tiles[i]) continue;
+          ok = tc::mbar_wait(&bars->p_full[i], t & 1, abort_flag);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint64_t vd = v_desc + (uint64_t)((uint32_t)(vs * L::kTile) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)  // 16 keys: 8 columns of P, 16 value rows of 128 B
+            mma_bf16_ts(tmem + kO + (uint32_t)(D * i), tmem + (uint32_t)(128 * i + 8 * ks),
+                        vd + (uint64_t)((uint32_t)(ks * 16 * 128) >> 4), id_o, (t > 0 || ks > 0) ? 1u : 0u);
+          if (t + 1 < n_tiles[i])
+            logits(i, t + 1);
+          else
+            tc::mma_commit(&bars->o_done[i]);
+        }
+        if (!ok) break;
+        tc::mma_commit(&bars->empty[vs]);  // V(t) is read
+        if (t + 1 < nt) tc::mma_commit(&bars->empty[(vj + 1) % L::kStages]);  // and K(t + 1)
+      }
+      tc::mma_commit(&bars->mma_done);  // every MMA issued above has completed before TMEM is freed
+      tc::mbar_drain(&bars->mma_done, 0);
+    }
+  } else if (warp < 4) {
+    // ---- value check: the tiles in which some row masks a key
+    constexpr int kVec = L::kTile / 16;
+    for (int t = t_mask; t < nt; ++t) {
+      const int j = 2 * t + 1, s = j % L::kStages;
+      if (!tc::mbar_wait(&bars->full[s], (j / L::kStages) & 1, abort_flag)) break;
+      uint4* tile = reinterpret_cast<uint4*>(sm + L::kRing + s * L::kTile);
+      uint32_t top = 0;  // the largest magnitude, per 16-bit half
+#pragma unroll 8
+      for (int i = tid - 64; i < kVec; i += 64) {
+        const uint4 w = tile[i];
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                     __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+      }
+      if ((top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u) {
+        bars->dirty = 1;
+        for (int i = tid - 64; i < kVec; i += 64) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(tile + i);
+          for (int u = 0; u < 4; ++u) {
+            uint32_t x = w[u];
+            if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+            if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
+            w[u] = x;
+          }
+        }
+        tc::fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->clean[t - t_mask]);
+    }
+  } else {
+    // ---- softmax of one MMA tile, one row per thread
+    const int i = (warp - 4) >> 2, wq = warp & 3;
+    const int r = 32 * wq + lane;
+    const int ti = i * a.nt + r / a.G;  // token of this row in the block
+    const int h = g * a.G + r % a.G;
+    const bool mine = seq >= 0 && r < a.nt * a.G && ti < lq - i0;
+    const int limit = std::min(ti, lq - i0 - 1) + i0 + lk - lq;  // last key the row sees
+    const int64_t row = (int64_t)(q0 + i0) + ti;                 // its row of out and lse
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * wq) << 16);
+    const uint32_t s_col = lane_base + (uint32_t)(128 * i), o_col = lane_base + kO + (uint32_t)(D * i);
+    float m_ref = -INFINITY;
+    double l = 0.0;
+    bool ok = true;
+    for (int t = 0; t < n_tiles[i]; ++t) {
+      if (!tc::mbar_wait(&bars->s_full[i], t & 1, abort_flag)) { ok = false; break; }
+      __syncwarp();
+      tc::tc_fence_after();
+      uint32_t x[128];
+      {
+        uint32_t* x1 = x + 64;
+        KVC_TMEM_LD64(s_col, x);
+        KVC_TMEM_LD64(s_col + 64u, x1);
+        KVC_TMEM_WAIT_LD64(x);
+        KVC_TMEM_TIE32(x1);
+        uint32_t* x2 = x + 96;
+        KVC_TMEM_TIE32(x2);
+      }
+      if (t >= t_mask) {
+        const int lim = limit - t * kVT;  // the last visible column
+#pragma unroll
+        for (int e = 0; e < kVT; ++e)
+          if (e > lim) x[e] = __float_as_uint(-INFINITY);
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kVT; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
+      const float mc = mx * a.c;
+      const bool move = mc > m_ref + kVSlack || (m_ref == -INFINITY && mc > -INFINITY);
+      float alpha = 1.f;
+      if (move) {
+        alpha = m_ref == -INFINITY ? 0.f : tc::ex2_approx(m_ref - mc);
+        l *= (double)alpha;
+        m_ref = mc;
+      }
+      if (t > 0 && __any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
+          KVC_TMEM_WAIT_LD32(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st32(o_col + (uint32_t)c0, o);
+        }
+      }
+      // a row that has seen no key yet has only x = -inf: p = 2^-inf = 0
+      const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+      const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+          const int e = 64 * half + 2 * u;
+          const float2 y = tc::fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, nm2);
+          const float2 p = make_float2(tc::ex2_approx(y.x), tc::ex2_approx(y.y));
+          sum[u & 1] = tc::add2(sum[u & 1], p);
+          const __nv_bfloat162 hp = __floats2bfloat162_rn(p.x, p.y);
+          w[u] = *reinterpret_cast<const uint32_t*>(&hp);
+        }
+        tmem_st32(s_col + (uint32_t)(32 * half), w);
+      }
+      const float2 s2 = tc::add2(sum[0], sum[1]);
+      l += (double)(s2.x + s2.y);
+      tmem_wait_st();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->p_full[i]);
+    }
+    // ---- the output rows and log-sum-exp
+    if (ok && n_tiles[i] > 0) ok = tc::mbar_wait(&bars->o_done[i], 0, abort_flag);
+    __syncwarp();
+    if (ok && seq >= 0) {
+      tc::tc_fence_after();
+      const bool seen = limit >= 0;  // no key otherwise
+      const float inv = seen ? (float)(1.0 / l) : 0.f;
+      const bool dirty = *(volatile int*)&bars->dirty != 0;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t o[32];
+        if (n_tiles[i] > 0) {
+          KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
+          KVC_TMEM_WAIT_LD32(o);
+        }
+        if (!mine || !a.out) continue;
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = seen ? __uint_as_float(o[e]) * inv : 0.f;
+        if (dirty)  // non-finite values of the checked tiles, where this row sees them
+          for (int j = t_mask * kVT; j <= limit; ++j) {
+            const uint16_t* vr = a.v + (int64_t)(k0 + j) * a.v_sn + (int64_t)g * a.v_sh + c0;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t bits = vr[e];
+              if ((bits & 0x7F80u) == 0x7F80u) f[e] += __uint_as_float(bits << 16);
+            }
+          }
+        uint4* dst = reinterpret_cast<uint4*>(a.out + (row * a.H + h) * D + c0);
+#pragma unroll
+        for (int v8 = 0; v8 < 4; ++v8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const __nv_bfloat162 hp = __floats2bfloat162_rn(f[8 * v8 + 2 * u], f[8 * v8 + 2 * u + 1]);
+            w[u] = *reinterpret_cast<const uint32_t*>(&hp);
+          }
+          dst[v8] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      if (mine && a.lse)
+        a.lse[row * a.H + h] = seen ? (float)(((double)m_ref + log2(l)) * kLn2) : -INFINITY;
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && tid == 0) {
+    set_dev_err(a.err, KVC_DEV_ERR_TIMEOUT);
+    if (issued > 0) tc::mbar_drain(&bars->qfull, 0);
+    for (int j = std::max(0, issued - L::kStages); j < issued; ++j)
+      tc::mbar_drain(&bars->full[j % L::kStages], (j / L::kStages) & 1);
+  }
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &qr) == cudaSuccess &&
+        qr == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// 3-D map over a strided [n][heads][d] bf16 tensor: boxes of 64 columns x box_h heads x box_n rows.
+kvc_status make_map(CUtensorMap* m, const uint16_t* base, int d, int heads, int64_t n, int64_t sn, int64_t sh, int box_h,
+                    int box_n) {
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)n};
+  cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)sn * 2};
+  cuuint32_t box[3] = {64u, (cuuint32_t)box_h, (cuuint32_t)box_n};
+  cuuint32_t es[3] = {1u, 1u, 1u};
+  if (heads == 1) strides[0] = (cuuint64_t)d * 2;  // a size-1 dimension still needs a legal stride
+  if (n == 1) strides[1] = (cuuint64_t)d * 2;
+  if (encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled failed for the prefill operands");
+  return KVC_OK;
+}
+
+kvc_status check_varlen(int32_t H, int32_t Hkv, int32_t d, int32_t batch, int64_t total_q, int64_t max_q,
+                        int64_t max_k) {
+  if (d != 64 && d != 128) return fail(KVC_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  KVC_CHECK_ARG(H >= 1 && Hkv >= 1 && H % Hkv == 0, "num_heads must be a positive multiple of num_kv_heads");
+  if (H / Hkv > kVT) return fail(KVC_ERR_UNSUPPORTED, "at most 128 query heads per KV head");
+  KVC_CHECK_ARG(batch >= 1 && batch <= 1024, "batch must be in 1..1024");
+  KVC_CHECK_ARG(total_q >= 0 && total_q < (int64_t(1) << 31), "need 0 <= total_q < 2^31");
+  KVC_CHECK_ARG(max_q >= 0 && max_k >= 0 && max_q < (int64_t(1) << 31) && max_k < (int64_t(1) << 31),
+                "need 0 <= max_seqlen < 2^31");
+  return KVC_OK;
+}
+
+template <int D>
+kvc_status launch_varlen(dim3 grid, cudaStream_t st, const CUtensorMap (&maps)[3], const VarArgs& a) {
+  static ContextCache cache;
+  const kvc_status s = once_per_context(cache, [] {
+    KVC_CUDA_TRY(cudaFuncSetAttribute(prefill_varlen_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)VarSmem<D>::kBytes));
+    return KVC_OK;
+  });
+  if (s != KVC_OK) return s;
+  const Launch l(grid, dim3(kVBlock), VarSmem<D>::kBytes, st);
+  KVC_CUDA_TRY(l.run(prefill_varlen_kernel<D>, maps[0], maps[1], maps[2], a));
+  count_launch();
+  return KVC_OK;
+}
+
+}  // namespace
+}  // namespace kvc
+
+using namespace kvc;
+
+extern "C" kvc_status kvc_prefill_varlen_workspace_size(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                                        int32_t batch, int64_t total_q, int64_t max_seqlen_q,
+                                                        int64_t max_seqlen_k, size_t* bytes) {
+  clear_error();
+  const kvc_status s = check_varlen(num_heads, num_kv_heads, head_dim, batch, total_q, max_seqlen_q, max_seqlen_k);
+  if (s != KVC_OK) return s;
+  KVC_CHECK_ARG(bytes != nullptr, "bytes must be non-NULL");
+  *bytes = 0;
+  return KVC_OK;
+}
+
+extern "C" kvc_status kvc_prefill_attention_varlen(
+    const uint16_t* q, int64_t q_stride_n, int64_t q_stride_h, const uint16_t* k, int64_t k_stride_n,
+    int64_t k_stride_h, const uint16_t* v, int64_t v_stride_n, int64_t v_stride_h, const int32_t* cu_seqlens_q,
+    const int32_t* cu_seqlens_k, int32_t batch, int64_t total_q, int64_t total_k, int64_t max_seqlen_q,
+    int64_t max_seqlen_k, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, float scale, uint16_t* out,
+    float* lse, void* ws, size_t ws_bytes, int32_t* dev_err, void* stream) {
+  clear_error();
+  kvc_status s = check_varlen(num_heads, num_kv_heads, head_dim, batch, total_q, max_seqlen_q, max_seqlen_k);
+  if (s != KVC_OK) return s;
+  KVC_CHECK_ARG(q && k && v && cu_seqlens_q && cu_seqlens_k, "q, k, v and the cu_seqlens must be non-NULL");
+  KVC_CHECK_ARG(total_k >= 1 && total_k < (int64_t(1) << 31), "need 1 <= total_k < 2^31");
+  KVC_CHECK_ARG(scale > 0.f && scale < 1e30f, "scale must be positive and finite");
+  KVC_CHECK_ARG(aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && (!out || aligned(out, 16)),
+                "q, k, v and out must be 16-byte aligned");
+  for (const int64_t st : {q_stride_n, q_stride_h, k_stride_n, k_stride_h, v_stride_n, v_stride_h})
+    KVC_CHECK_ARG(st >= head_dim && st % 8 == 0 && st < (int64_t(1) << 36),
+                  "strides must be multiples of 8 elements, at least head_dim");
+  if (total_q == 0) return KVC_OK;  // no row to write
+  if (!encode_fn()) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  VarArgs a{};
+  a.v = v;
+  a.v_sn = v_stride_n;
+  a.v_sh = v_stride_h;
+  a.cu_q = cu_seqlens_q;
+  a.cu_k = cu_seqlens_k;
+  a.total_q = total_q;
+  a.total_k = total_k;
+  a.max_q = max_seqlen_q;
+  a.max_k = max_seqlen_k;
+  a.batch = batch;
+  a.H = num_heads;
+  a.Hkv = num_kv_heads;
+  a.G = num_heads / num_kv_heads;
+  a.nt = kVT / a.G;
+  a.c = (float)((double)scale * kLog2e);
+  a.out = out;
+  a.lse = lse;
+  a.err = dev_err;
+  CUtensorMap maps[3];
+  s = make_map(&maps[0], q, head_dim, num_heads, total_q, q_stride_n, q_stride_h, a.G, a.nt);
+  if (s == KVC_OK) s = make_map(&maps[1], k, head_dim, num_kv_heads, total_k, k_stride_n, k_stride_h, 1, kVT);
+  if (s == KVC_OK) s = make_map(&maps[2], v, head_dim, num_kv_heads, total_k, v_stride_n, v_stride_h, 1, kVT);
+  if (s != KVC_OK) return s;
+  // blocks of all sequences: at most one that is not full per sequence
+  const int64_t per = 2 * a.nt;
+  const int64_t blocks = std::min(total_q / per + batch, (int64_t)batch * ((max_seqlen_q + per - 1) / per));
+  if (blocks == 0) return KVC_OK;
+  KVC_CHECK_ARG(blocks * num_kv_heads < (int64_t(1) << 31), "too many query blocks for one call");
+  const dim3 grid((unsigned)(blocks * num_kv_heads));
+  const cudaStream_t st = (cudaStream_t)stream;
+  return head_dim == 128 ? launch_varlen<128>(grid, st, maps, a) : launch_varlen<64>(grid, st, maps, a);
+}
