@@ -82,7 +82,7 @@ struct VarSmem {
 struct VarBars {
   uint64_t qfull, full[8], empty[8];
   uint64_t s_full[2], p_full[2], o_done[2];
-  uint64_t clean[kVMaxClean];
+  uint64_t vland[kVMaxClean], clean[kVMaxClean];  // value tiles to be checked: landed, checked (used once each)
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort, dirty;
@@ -159,7 +159,10 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       tc::mbar_init(&bars->p_full[i], 4);
       tc::mbar_init(&bars->o_done[i], 1);
     }
-    for (int i = 0; i < kVMaxClean; ++i) tc::mbar_init(&bars->clean[i], 2);
+    for (int i = 0; i < kVMaxClean; ++i) {
+      tc::mbar_init(&bars->vland[i], 1);
+      tc::mbar_init(&bars->clean[i], 2);
+    }
     tc::mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
     bars->dirty = 0;
@@ -243,10 +246,16 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       for (int j = 0; j < 2 * nt; ++j) {
         const int s = j % L::kStages;
         if (j >= L::kStages && !tc::mbar_wait(&bars->empty[s], ((j / L::kStages) - 1) & 1, abort_flag)) break;
-        tc::mbar_arrive_expect_tx(&bars->full[s], (uint32_t)L::kTile);
+        // a value tile to be checked lands on a barrier of its own, which its
+        // readers can wait for without following the ring's phases
+        const int t = j >> 1;
+        const bool checked = (j & 1) && t >= t_mask;
+        uint64_t* land = checked ? &bars->vland[t - t_mask] : &bars->full[s];
+        if (checked) tc::mbar_arrive(&bars->full[s]);
+        tc::mbar_arrive_expect_tx(land, (uint32_t)L::kTile);
         for (int cb = 0; cb < kCB; ++cb)
-          tc::tma_load_3d(sm + L::kRing + s * L::kTile + cb * L::kBlk, (j & 1) ? &vmap : &kmap, &bars->full[s],
-                          cb * 64, g, k0 + (j >> 1) * kVT);
+          tc::tma_load_3d(sm + L::kRing + s * L::kTile + cb * L::kBlk, (j & 1) ? &vmap : &kmap, land, cb * 64, g,
+                          k0 + t * kVT);
         issued = j + 1;
       }
     }
@@ -309,8 +318,8 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     // ---- value check: the tiles in which some row masks a key
     constexpr int kVec = L::kTile / 16;
     for (int t = t_mask; t < nt; ++t) {
-      const int j = 2 * t + 1, s = j % L::kStages;
-      if (!tc::mbar_wait(&bars->full[s], (j / L::kStages) & 1, abort_flag)) break;
+      const int s = (2 * t + 1) % L::kStages;
+      if (!tc::mbar_wait(&bars->vland[t - t_mask], 0, abort_flag)) break;
       uint4* tile = reinterpret_cast<uint4*>(sm + L::kRing + s * L::kTile);
       uint32_t top = 0;  // the largest magnitude, per 16-bit half
 #pragma unroll 8
@@ -466,7 +475,10 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     set_dev_err(a.err, KVC_DEV_ERR_TIMEOUT);
     if (issued > 0) tc::mbar_drain(&bars->qfull, 0);
     for (int j = std::max(0, issued - L::kStages); j < issued; ++j)
-      tc::mbar_drain(&bars->full[j % L::kStages], (j / L::kStages) & 1);
+      if ((j & 1) && (j >> 1) >= t_mask)
+        tc::mbar_drain(&bars->vland[(j >> 1) - t_mask], 0);
+      else
+        tc::mbar_drain(&bars->full[j % L::kStages], (j / L::kStages) & 1);
   }
   if (warp == 1) {
     tc::tc_fence_after();

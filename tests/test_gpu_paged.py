@@ -183,6 +183,30 @@ def test_prefill_varlen_agrees_with_the_single_sequence_call():
     assert torch.equal(again, out) and torch.equal(lse2, lse)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_varlen_long_rows_after_non_finite_memory(d):
+    """Long prompts (the K/V ring goes round many times), and shared memory
+    full of NaN from the call before: every row against the plain fp64 form."""
+    rng = np.random.default_rng(d + 1)
+    n, H = 5000, 2
+    q, qd = _bf16(rng, n, H, d)
+    k, kd = _bf16(rng, n, 1, d)
+    v, vd = _bf16(rng, n, 1, d)
+    nan = torch.full_like(vd, float("nan"))
+    _run_prefill(torch.full_like(qd, float("nan")), nan, nan, [n], [n])
+    out, lse = _run_prefill(qd, kd, vd, [n], [n])
+    t = [torch.from_numpy(x).cuda().transpose(0, 1) for x in (q, k, v)]
+    s = t[0] @ t[1].transpose(1, 2) / math.sqrt(d)
+    s.masked_fill_(torch.ones(n, n, dtype=torch.bool, device="cuda").triu(1), -math.inf)
+    z = torch.logsumexp(s, 2)
+    p = (s - z[..., None]).exp()
+    size = (p @ t[2].abs()).transpose(0, 1).cpu().numpy()
+    # E of the module's tolerances with |q|, |k| at their largest norms
+    E = (d + 4) * 2.0 ** -23 / math.sqrt(d) * np.linalg.norm(q, axis=2).max() * np.linalg.norm(k, axis=2).max() + 2e-5
+    _close(_np(lse), z.t().cpu().numpy(), np.full((n, H), E + 1e-5), "lse")
+    _close(_np(out), (p @ t[2]).transpose(0, 1).cpu().numpy(), (2.02 * 2.0 ** -8 + 2 * E) * size, "out")
+
+
 def test_prefill_varlen_many_sequences():
     """More sequences than a warp holds, some empty, in one call."""
     rng = np.random.default_rng(29)
