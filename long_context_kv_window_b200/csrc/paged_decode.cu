@@ -5,7 +5,35 @@
 // 2.A: attention accumulated per token.  With entry j of KV head g in page
 // table[j / page], and query head h of the group:
 //     s_j = scale * q_h . k_j,  out_h = sum_j exp(s_j - lse_h) v_j,  weights_j += sum_h exp(s_j - lse_h).
+//
+// A stream from HBM (4 d bytes per entry, 4 G d operations on them).  The
+// entries of all (sequence, KV head) pairs form one row of 64-entry tiles,
+// which is cut into equal runs, one per CTA, whatever the sequences' lengths:
+// a ragged batch loads every SM alike.  A run covers pieces of one or more
+// pairs; a pair that lies in one run is finished there, the others leave
+// (max, sum, output) per run and the last of their CTAs joins them in run
+// order (a ticket counter per pair, returned to zero).
+//
+// Every warp streams its own 16 entries of each tile (one page holds them)
+// through a ring of its own -- TMA boxes, 128-byte swizzle, requested by the
+// warp itself -- and shares nothing with the other warps until a pair ends,
+// so no barrier joins them in the loop.  Both contractions are mma.sync: the
+// logits S[head][entry] (M = 16 heads, the group's and zero rows) come out in
+// the layout in which the second one takes P, so P stays in registers, which
+// the tcgen05 form cannot do; at 4 d bytes per entry the legacy tensor rate is
+// many times what the stream needs.  P enters as two bf16 terms (hi + lo, good
+// to 2^-17); up to 8 heads per group both ride in one MMA, hi in rows 0..7 and
+// lo in rows 8..15.  Row maxima are references that move only when a logit
+// passes them by more than 8 log2 units (a warp vote; p <= 2^8 otherwise).
+//
+// With `accumulate` the logits go to the workspace (4 G bytes per entry, which
+// stay in L2 for most sizes) and a second kernel adds exp(s - lse) to the
+// weights once the log-sum-exp is known.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <mutex>
 
 #include <cuda_bf16.h>
 
@@ -15,9 +43,14 @@
 namespace kvc {
 namespace {
 
-constexpr int kPdThreads = 256;
-constexpr int kPdWarps = kPdThreads / 32;
+constexpr int kPdWarps = 4;
+constexpr int kPdThreads = 32 * kPdWarps;
+constexpr int kPdUnit = 16;                  // entries a warp takes at a time
+constexpr int kPdTile = kPdUnit * kPdWarps;  // entries of a tile
 constexpr int kPdMaxG = 16;
+constexpr int kPdCtasPerSm = 2;
+constexpr int kPdMaxBatch = 1024;
+constexpr float kPdSlack = 8.f;
 constexpr double kLog2e = 1.4426950408889634;
 constexpr double kLn2 = 0.6931471805599453;
 
@@ -27,94 +60,527 @@ struct PdArgs {
   int64_t q_sb, q_sh;
   int H, G;
   float c2;  // scale * log2(e)
-  int64_t max_len;
-  int accumulate;
+  int64_t max_len, ld;  // ld: max_len rounded up to whole units
   float* out;     // [B][H][d]
   float* lse;     // [B][H] or nullptr
-  float* logits;  // [B][H][max_len], log2 domain (accumulate)
+  float* z;       // [B][H]: log-sum-exp in log2 units (accumulate; else nullptr)
+  float* logits;  // [B][H][ld], log2 units (accumulate)
+  uint32_t* tickets;  // [B*Hkv]: runs of the pair done
+  float* part_ml;     // [2 * runs][G][2]: max, sum (sum -1: a page id was outside the pool)
+  float* part_o;      // [2 * runs][G][d]
   int32_t* err;
 };
 
-// CTA (KV head, sequence); entry j belongs to warp j % 8, its lanes hold D/32
-// dimensions each, with one online softmax per head and warp.
-template <int D>
-__global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const PdArgs a) {
-  constexpr int kDL = D / 32;
-  extern __shared__ float sm[];  // [warps][G]: max, sum; [warps][G][D]: output rows
-  __shared__ int bad;
+// D: head_dim; G16: more than 8 heads per group.
+template <int D, bool G16>
+struct PdSmem {
+  static constexpr int kRows = G16 ? 16 : 8;
+  static constexpr int kBox = kPdUnit * 128;            // 16 entries x 64 columns (2 KB)
+  static constexpr int kMat = (D / 64) * kBox;          // 16 entries of k or v
+  static constexpr int kStage = 2 * kMat;
+  static constexpr int kStages = D == 64 ? 6 : G16 ? 2 : 3;
+  static constexpr int kRing = kPdWarps * kStages * kStage;
+  static constexpr int kMerge = 2 * kRows * (D + 4) * 4;  // two warps' rows at a time
+  static constexpr size_t kBytes = 1024 + (size_t)kRing + kMerge + (kPdMaxBatch + 1) * 4 + 512;
+  static_assert(kPdCtasPerSm * (kBytes + 1024) <= 233472, "CTAs per SM");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(tc::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+// (x, y) as bf16 pairs hi + lo
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  const float2 f = __bfloat1622float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_bf16(x - f.x, y - f.y);
+}
+
+// The runs: pair p = (b, g) holds tiles [first(p), first(p) + nu(b)) of the
+// row of all tiles; run i holds [total * i / runs, total * (i + 1) / runs).
+struct Runs {
+  int64_t total;
+  int runs;
+  __device__ __forceinline__ int64_t start(int i) const { return total * i / runs; }
+  // the run that holds tile x
+  __device__ __forceinline__ int of(int64_t x) const { return (int)(((x + 1) * runs + total - 1) / total) - 1; }
+};
+
+// A piece of a pair inside a run.
+struct Piece {
+  int b, g;
+  int len, nu;  // entries and tiles of the pair
+  int t0, t1;   // tiles of the piece
+};
+
+template <int D, bool G16>
+__global__ void __launch_bounds__(kPdThreads, kPdCtasPerSm)
+paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PdArgs a) {
+  using L = PdSmem<D, G16>;
+  constexpr int kRows = L::kRows, kKS = D / 16, kNT = D / 8;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* merge = reinterpret_cast<float*>(sm + L::kRing);                       // [2][kRows][D + 4]
+  int* first = reinterpret_cast<int*>(sm + L::kRing + L::kMerge);              // [B + 1]: tiles before sequence b (per head)
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kRing + L::kMerge + (kPdMaxBatch + 2) / 2 * 8);  // [warps][stages]
+  int* flags = reinterpret_cast<int*>(full + kPdWarps * L::kStages);           // abort, last, warp totals, warps' bad flags
+  volatile int* abort_flag = flags;
+  const Paged& c = a.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.G, B = c.batch, Hkv = c.Hkv;
+
+  if (tid == 0) {
+    for (int i = 0; i < kPdWarps * L::kStages; ++i) tc::mbar_init(&full[i], 1);
+    flags[0] = 0;
+    tc::fence_mbar_init();
+    tc::prefetch_tmap(&kmap);
+    tc::prefetch_tmap(&vmap);
+  }
+  pdl_wait();  // the cache and q may come from the previous kernels of the stream
+  // ---- tiles before each sequence
+  {
+    const int per = (B + kPdThreads - 1) / kPdThreads, b0 = tid * per;
+    int mine = 0;
+    for (int u = 0; u < per; ++u) {
+      const int b = b0 + u;
+      if (b >= B) break;
+      const int n = c.seq_lens[b];
+      mine += n > 0 && n <= a.max_len ? (n + kPdTile - 1) / kPdTile : 0;
+    }
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) flags[2 + warp] = inc;
+    __syncthreads();
+    int at = inc - mine;
+    for (int w = 0; w < warp; ++w) at += flags[2 + w];
+    for (int u = 0; u < per; ++u) {
+      const int b = b0 + u;
+      if (b >= B) break;
+      first[b] = at;
+      const int n = c.seq_lens[b];
+      at += n > 0 && n <= a.max_len ? (n + kPdTile - 1) / kPdTile : 0;
+      if (b == B - 1) first[B] = at;
+    }
+    __syncthreads();
+  }
+  // ---- sequences without entries (or with a length that cannot be), dealt out over the CTAs
+  for (int b = blockIdx.x; b < B; b += gridDim.x) {
+    if (first[b + 1] != first[b]) continue;
+    if (tid == 0 && c.seq_lens[b] != 0) set_dev_err(a.err, KVC_DEV_ERR_PAGES);
+    for (int i = tid; i < a.H * D; i += kPdThreads) a.out[(int64_t)b * a.H * D + i] = 0.f;
+    for (int h = tid; h < a.H; h += kPdThreads) {
+      if (a.lse) a.lse[(int64_t)b * a.H + h] = -INFINITY;
+      if (a.z) a.z[(int64_t)b * a.H + h] = -INFINITY;
+    }
+  }
+  Runs rs;
+  rs.total = (int64_t)first[B] * Hkv;
+  rs.runs = (int)std::min<int64_t>(gridDim.x, rs.total);
+  const int run = blockIdx.x;
+  if (run >= rs.runs) return;
+  const int64_t x0 = rs.start(run), x1 = rs.start(run + 1);
+
+  // the piece of the run [x, x1) that starts at x
+  auto piece_at = [&](int64_t x) {
+    Piece p;
+    int lo = 0, hi = B - 1;  // the last sequence whose tiles begin at or before x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((int64_t)first[mid] * Hkv <= x) lo = mid; else hi = mid - 1;
+    }
+    p.b = lo;
+    p.nu = first[lo + 1] - first[lo];
+    const int64_t r = x - (int64_t)first[lo] * Hkv;
+    p.g = (int)(r / p.nu);
+    p.t0 = (int)(r % p.nu);
+    p.t1 = (int)std::min<int64_t>(p.nu, p.t0 + (x1 - x));
+    p.len = c.seq_lens[p.b];
+    return p;
+  };
+
+  // ---- producer state of this warp: the next unit to request
+  uint8_t* ring = sm + (size_t)warp * L::kStages * L::kStage;
+  const uint32_t ring_u32 = tc::smem_u32(ring);
+  uint64_t* bar = full + warp * L::kStages;
+  Piece pp = piece_at(x0);
+  int64_t px = x0;       // tile index of the piece's end so far: px + (pp.t1 - pp.t0) is the next piece's start
+  int pt = pp.t0;        // next tile of the piece
+  int page_base = -32;   // tile of lane 0's page id
+  int page_id = 0;
+  unsigned issued = 0;   // units requested
+  uint32_t bad_units = 0;  // bit s: the unit in stage s had a page id outside the pool
+  auto request = [&]() {  // requests this warp's next unit, if the run has one; warp-uniform
+    for (;;) {
+      if (pt >= pp.t1) {
+        px += pp.t1 - pp.t0;
+        if (px >= x1) return;
+        pp = piece_at(px);
+        pt = pp.t0;
+        page_base = -32;
+      }
+      if (pt * kPdTile + warp * kPdUnit < pp.len) break;
+      ++pt;  // the last tile of a pair: no entry for this warp
+    }
+    if (pt >= page_base + 32 || page_base < 0) {  // page ids of the next 32 tiles
+      page_base = pt;
+      const int64_t s = (int64_t)(pt + lane) * kPdTile + warp * kPdUnit;
+      page_id = pt + lane < pp.t1 && s < pp.len ? c.page_of(pp.b, s) : 0;
+    }
+    const int p = __shfl_sync(0xffffffffu, page_id, pt - page_base);
+    const int s = (int)(issued % L::kStages);
+    bad_units = p < 0 ? bad_units | 1u << s : bad_units & ~(1u << s);
+    if (lane == 0) {
+      tc::mbar_arrive_expect_tx(&bar[s], (uint32_t)L::kStage);
+      const int slot = (pt * kPdTile + warp * kPdUnit) & (c.page - 1), at = p < 0 ? c.num_pages : p;  // past the pool: zeros
+      const uint32_t dst = ring_u32 + (uint32_t)(s * L::kStage);
+#pragma unroll
+      for (int cb = 0; cb < D / 64; ++cb) {
+        tma_load_4d(dst + cb * L::kBox, &kmap, &bar[s], cb * 64, slot, pp.g, at);
+        tma_load_4d(dst + L::kMat + cb * L::kBox, &vmap, &bar[s], cb * 64, slot, pp.g, at);
+      }
+    }
+    ++issued;
+    ++pt;
+  };
+  for (int i = 0; i < L::kStages; ++i) request();
+
+  // ---- the run, piece by piece
+  const int row = lane >> 2, col = 2 * (lane & 3);  // accumulator rows row, row + 8 and columns col, col + 1
+  // ldmatrix rows: K 8 entries x 4 pieces of 8 columns; V two blocks of 8 entries x two of 8 columns
+  const int k_row = lane & 7, k_piece = lane >> 3;
+  const int v_row = lane & 15, v_piece = lane >> 4;
+  unsigned taken = 0;
+  for (int64_t x = x0; x < x1;) {
+    const Piece p = piece_at(x);
+    x += p.t1 - p.t0;
+    const int64_t qb = (int64_t)p.b * a.q_sb + (int64_t)p.g * G * a.q_sh;
+    uint32_t qa[kKS][2], qc[G16 ? kKS : 1][2];  // Q rows row (and row + 8) as MMA A operand
+#pragma unroll
+    for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int k = ks * 16 + 8 * u + col;
+        qa[ks][u] = row < G ? *reinterpret_cast<const uint32_t*>(a.q + qb + (int64_t)row * a.q_sh + k) : 0u;
+        if constexpr (G16)
+          qc[ks][u] = row + 8 < G ? *reinterpret_cast<const uint32_t*>(a.q + qb + (int64_t)(row + 8) * a.q_sh + k) : 0u;
+      }
+    float o[kNT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    bool bad = false;
+    for (int t = p.t0; t < p.t1; ++t) {
+      const int s0 = t * kPdTile + warp * kPdUnit;  // first entry of the unit
+      if (s0 >= p.len) break;
+      const int st = (int)(taken % L::kStages);
+      if (!tc::mbar_wait(&bar[st], (taken / L::kStages) & 1, abort_flag)) break;
+      __syncwarp();
+      const uint32_t kt = ring_u32 + (uint32_t)(st * L::kStage), vt = kt + L::kMat;
+      bad |= (bad_units >> st) & 1;
+      const int left = p.len - s0;  // valid entries of the unit, if below 16
+      if (left < kPdUnit) {  // what lies behind the entries must not meet p = 0 as infinity or NaN
+        for (int i = lane; i < (kPdUnit - left) * (D / 8); i += 32) {
+          const int r = left + i / (D / 8), pc = i % (D / 8);
+          *reinterpret_cast<uint4*>(ring + st * L::kStage + L::kMat + (pc >> 3) * L::kBox + r * 128 + (pc & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        tc::fence_proxy_async_smem();  // before the stage's next copy
+        __syncwarp();
+      }
+      // logits of 16 entries: two 8-entry column blocks
+      float sc[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+#pragma unroll
+        for (int k4 = 0; k4 < D / 32; ++k4) {
+          const int r = 8 * n + k_row, pc = 4 * k4 + k_piece;  // 16-byte piece of the row
+          uint32_t b[4];
+          ldsm4(b, kt + (uint32_t)((pc >> 3) * L::kBox + r * 128 + (((pc & 7) ^ (r & 7)) << 4)));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int ks = 2 * k4 + u;
+            if constexpr (G16)
+              mma_16816(sc[n], qa[ks][0], qc[ks][0], qa[ks][1], qc[ks][1], b[2 * u], b[2 * u + 1]);
+            else
+              mma_16816(sc[n], qa[ks][0], 0u, qa[ks][1], 0u, b[2 * u], b[2 * u + 1]);
+          }
+        }
+      }
+      constexpr int kHalf = G16 ? 2 : 1;  // accumulator row halves in use
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2 * kHalf; ++e) {
+          const bool valid = 8 * n + col + (e & 1) < left;
+          sc[n][e] = valid ? sc[n][e] * a.c2 : -INFINITY;
+          mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
+        }
+      if (a.logits) {
+#pragma unroll
+        for (int hf = 0; hf < kHalf; ++hf)
+          if (row + 8 * hf < G) {
+            float* dst = a.logits + ((int64_t)p.b * a.H + p.g * G + row + 8 * hf) * a.ld + s0 + col;
+            *reinterpret_cast<float2*>(dst) = make_float2(sc[0][2 * hf], sc[0][2 * hf + 1]);
+            *reinterpret_cast<float2*>(dst + 8) = make_float2(sc[1][2 * hf], sc[1][2 * hf + 1]);
+          }
+      }
+      bool move = mx[0] > m[0] + kPdSlack || (m[0] == -INFINITY && mx[0] > -INFINITY);
+      if constexpr (G16) move |= mx[1] > m[1] + kPdSlack || (m[1] == -INFINITY && mx[1] > -INFINITY);
+      if (__any_sync(0xffffffffu, move)) {
+        float al[2] = {1.f, 1.f};
+#pragma unroll
+        for (int hf = 0; hf < kHalf; ++hf) {
+          float v = mx[hf];
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+          if (v > m[hf]) {
+            al[hf] = m[hf] == -INFINITY ? 0.f : tc::ex2_approx(m[hf] - v);
+            m[hf] = v;
+          }
+          l[hf] *= al[hf];
+        }
+        if constexpr (!G16) al[1] = al[0];  // rows 8..15 hold the second terms of the same heads
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][e] *= al[e >> 1];
+      }
+      uint32_t hi[2][2], lo[2][2];  // [column block][row half]
+#pragma unroll
+      for (int hf = 0; hf < kHalf; ++hf) {
+        const float ref = m[hf] == -INFINITY ? 0.f : m[hf];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float p0 = tc::ex2_approx(sc[n][2 * hf] - ref), p1 = tc::ex2_approx(sc[n][2 * hf + 1] - ref);
+          l[hf] += p0 + p1;
+          split_bf16(p0, p1, hi[n][hf], lo[n][hf]);
+        }
+      }
+#pragma unroll
+      for (int d16 = 0; d16 < D / 16; ++d16) {
+        const int pc = 2 * d16 + v_piece;
+        uint32_t b[4];
+        ldsm4_t(b, vt + (uint32_t)((pc >> 3) * L::kBox + v_row * 128 + (((pc & 7) ^ (v_row & 7)) << 4)));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if constexpr (G16) {
+            mma_16816(o[2 * d16 + u], hi[0][0], hi[0][1], hi[1][0], hi[1][1], b[2 * u], b[2 * u + 1]);
+            mma_16816(o[2 * d16 + u], lo[0][0], lo[0][1], lo[1][0], lo[1][1], b[2 * u], b[2 * u + 1]);
+          } else {
+            mma_16816(o[2 * d16 + u], hi[0][0], lo[0][0], hi[1][0], lo[1][0], b[2 * u], b[2 * u + 1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      ++taken;
+      request();
+    }
+    // ---- join the four warps: 2 and 3 into 0 and 1, then 1 into 0 (rows of
+    // heads; the lanes of a quad hold the columns of a row)
+    if constexpr (!G16) {
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        o[n][0] += o[n][2];
+        o[n][1] += o[n][3];
+      }
+    }
+    constexpr int kHalf = G16 ? 2 : 1;
+#pragma unroll
+    for (int hf = 0; hf < kHalf; ++hf) {
+      l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
+      l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
+    }
+    if (lane == 0) flags[6 + warp] = bad;
+#pragma unroll 1
+    for (int half = kPdWarps / 2; half >= 1; half >>= 1) {
+      __syncthreads();
+      if (warp >= half && warp < 2 * half) {
+        float* dst = merge + (warp - half) * kRows * (D + 4);
+#pragma unroll
+        for (int hf = 0; hf < kHalf; ++hf) {
+          float* r = dst + (row + 8 * hf) * (D + 4);
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) *reinterpret_cast<float2*>(r + 8 * n + col) = make_float2(o[n][2 * hf], o[n][2 * hf + 1]);
+          if ((lane & 3) == 0) {
+            r[D] = m[hf];
+            r[D + 1] = l[hf];
+          }
+        }
+      }
+      __syncthreads();
+      if (warp < half) {
+        const float* src = merge + warp * kRows * (D + 4);
+#pragma unroll
+        for (int hf = 0; hf < kHalf; ++hf) {
+          const float* r = src + (row + 8 * hf) * (D + 4);
+          const float m2 = r[D], l2 = r[D + 1], M = fmaxf(m[hf], m2);
+          const float f1 = m[hf] == -INFINITY ? 0.f : tc::ex2_approx(m[hf] - M);
+          const float f2 = m2 == -INFINITY ? 0.f : tc::ex2_approx(m2 - M);
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) {
+            const float2 y = *reinterpret_cast<const float2*>(r + 8 * n + col);
+            o[n][2 * hf] = o[n][2 * hf] * f1 + y.x * f2;
+            o[n][2 * hf + 1] = o[n][2 * hf + 1] * f1 + y.y * f2;
+          }
+          l[hf] = l[hf] * f1 + l2 * f2;
+          m[hf] = M;
+        }
+      }
+    }
+    const bool whole = p.t0 == 0 && p.t1 == p.nu;
+    const int64_t h0 = (int64_t)p.b * a.H + p.g * G;  // first head of the pair
+    bad = flags[6] | flags[7] | flags[8] | flags[9];
+    if (bad && tid == 0) set_dev_err(a.err, KVC_DEV_ERR_PAGES);
+    if (warp == 0) {
+      const int slot = 2 * run + (p.t0 == 0 ? 1 : 0);
+#pragma unroll
+      for (int hf = 0; hf < kHalf; ++hf) {
+        const int h = row + 8 * hf;
+        if (h >= G) continue;
+        float* dst = whole ? a.out + (h0 + h) * D : a.part_o + ((int64_t)slot * G + h) * D;
+        const float f = !whole ? 1.f : bad ? 0.f : 1.f / l[hf];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+          *reinterpret_cast<float2*>(dst + 8 * n + col) =
+              bad ? make_float2(0.f, 0.f) : make_float2(o[n][2 * hf] * f, o[n][2 * hf + 1] * f);
+        if ((lane & 3) == 0) {
+          if (whole) {
+            const float z = bad ? -INFINITY : m[hf] + log2f(l[hf]);
+            if (a.lse) a.lse[h0 + h] = (float)((double)z * kLn2);
+            if (a.z) a.z[h0 + h] = z;
+          } else {
+            a.part_ml[((int64_t)slot * G + h) * 2] = m[hf];
+            a.part_ml[((int64_t)slot * G + h) * 2 + 1] = bad ? -1.f : l[hf];
+          }
+        }
+      }
+    }
+    if (whole) {
+      __syncthreads();  // the merge rows and flags are free again
+      continue;
+    }
+    // ---- the last run of the pair joins the pieces
+    const int64_t pair0 = x - (p.t1 - p.t0) - p.t0;  // the pair's first tile
+    const int c0 = rs.of(pair0), c1 = rs.of(pair0 + p.nu - 1);
+    __threadfence();
+    __syncthreads();
+    uint32_t* ticket = a.tickets + (int64_t)p.b * Hkv + p.g;
+    if (tid == 0) {
+      const bool last = atomicAdd(ticket, 1u) == (uint32_t)(c1 - c0);
+      if (last) *ticket = 0u;
+      flags[1] = last;
+    }
+    __syncthreads();
+    if (!flags[1]) continue;
+    __threadfence();
+    for (int h = warp; h < G; h += kPdWarps) {
+      // piece i is slot 1 of run c0 or slot 0 of run c0 + i
+      auto slot_of = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * G + h; };
+      const int np = c1 - c0 + 1;
+      float M = -INFINITY;
+      bool none = false;
+      for (int i = lane; i < np; i += 32) {
+        M = fmaxf(M, __ldcg(a.part_ml + slot_of(i) * 2));
+        none |= __ldcg(a.part_ml + slot_of(i) * 2 + 1) == -1.f;
+      }
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+      none = __any_sync(0xffffffffu, none);
+      float acc[D / 32], Ls = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < np; ++i) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + slot_of(i) * 2));
+        const float f = ml.x == -INFINITY ? 0.f : tc::ex2_approx(ml.x - M);
+        Ls += f * ml.y;
+        if constexpr (D == 128) {
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot_of(i) * D) + lane);
+          acc[0] += f * y.x;
+          acc[1] += f * y.y;
+          acc[2] += f * y.z;
+          acc[3] += f * y.w;
+        } else {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(a.part_o + slot_of(i) * D) + lane);
+          acc[0] += f * y.x;
+          acc[1] += f * y.y;
+        }
+      }
+      const float inv = 1.f / Ls;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) a.out[(h0 + h) * D + lane * (D / 32) + e] = none ? 0.f : acc[e] * inv;
+      if (lane == 0) {
+        const float z = none ? -INFINITY : M + log2f(Ls);
+        if (a.lse) a.lse[h0 + h] = (float)((double)z * kLn2);
+        if (a.z) a.z[h0 + h] = z;
+      }
+    }
+  }
+  if (*abort_flag) {  // a copy never landed: nothing of the stages may be in flight when the CTA leaves
+    for (unsigned i = issued > (unsigned)L::kStages ? issued - L::kStages : 0; i < issued; ++i)
+      if (lane == 0) tc::mbar_drain(&bar[i % L::kStages], (i / L::kStages) & 1);
+    if (lane == 0) set_dev_err(a.err, KVC_DEV_ERR_TIMEOUT);
+  }
+}
+
+// weights[j] += sum_h 2^(s_hj - z_h), heads in order: a thread per four entries.
+constexpr int kWtThreads = 256;
+__global__ void __launch_bounds__(kWtThreads) paged_weights_kernel(const PdArgs a) {
   pdl_wait();
   const Paged& c = a.c;
-  const int g = blockIdx.x, b = blockIdx.y, G = a.G;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t n = c.seq_lens[b];
-  if (tid == 0) bad = n < 0 || n > a.max_len;
-  __syncthreads();
-  if (!bad)
-    for (int64_t s = (int64_t)tid * c.page; s < n; s += (int64_t)kPdThreads * c.page)
-      if (c.page_of(b, s) < 0) bad = 1;
-  __syncthreads();
-  const int64_t len = bad ? 0 : n;
-  if (bad && tid == 0) set_dev_err(a.err, KVC_DEV_ERR_PAGES);
-  float* sm_m = sm;
-  float* sm_l = sm + kPdWarps * G;
-  float* sm_o = sm + 2 * kPdWarps * G;
-  for (int hl = 0; hl < G; ++hl) {
-    const int h = g * G + hl;
-    float q[kDL], o[kDL], m = -INFINITY, l = 0.f;
-    for (int e = 0; e < kDL; ++e) {
-      q[e] = __uint_as_float((uint32_t)a.q[(int64_t)b * a.q_sb + (int64_t)h * a.q_sh + lane * kDL + e] << 16);
-      o[e] = 0.f;
-    }
-    for (int64_t j = warp; j < len; j += kPdWarps) {
-      const int64_t row = c.row(c.page_of(b, j), g, j) + lane * kDL;
-      float s = 0.f;
-      for (int e = 0; e < kDL; ++e) s += q[e] * __uint_as_float((uint32_t)c.k[row + e] << 16);
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= a.c2;
-      if (a.accumulate && lane == 0) a.logits[((int64_t)b * a.H + h) * a.max_len + j] = s;
-      const float mn = fmaxf(m, s);
-      const float al = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(s - mn);
-      l = l * al + p;
-      for (int e = 0; e < kDL; ++e) o[e] = o[e] * al + p * __uint_as_float((uint32_t)c.v[row + e] << 16);
-      m = mn;
-    }
-    if (lane == 0) {
-      sm_m[warp * G + hl] = m;
-      sm_l[warp * G + hl] = l;
-    }
-    for (int e = 0; e < kDL; ++e) sm_o[(warp * G + hl) * D + lane * kDL + e] = o[e];
+  const int g = blockIdx.y, b = blockIdx.z;
+  const int n = c.seq_lens[b];
+  const int64_t s = ((int64_t)blockIdx.x * kWtThreads + threadIdx.x) * 4;
+  if (s >= n || n > a.max_len) return;
+  const int64_t h0 = (int64_t)b * a.H + (int64_t)g * a.G;
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int h = 0; h < a.G; ++h) {
+    const float z = __ldg(a.z + h0 + h);
+    if (z == -INFINITY) return;  // a sequence whose pages could not be read
+    const float4 x = *reinterpret_cast<const float4*>(a.logits + (h0 + h) * a.ld + s);
+    w[0] += tc::ex2_approx(x.x - z);
+    w[1] += tc::ex2_approx(x.y - z);
+    w[2] += tc::ex2_approx(x.z - z);
+    w[3] += tc::ex2_approx(x.w - z);
   }
-  __syncthreads();
-  for (int i = tid; i < G * D; i += kPdThreads) {
-    const int hl = i / D, e = i % D;
-    float M = -INFINITY, L = 0.f, O = 0.f;
-    for (int w = 0; w < kPdWarps; ++w) M = fmaxf(M, sm_m[w * G + hl]);
-    for (int w = 0; w < kPdWarps; ++w) {
-      const float mw = sm_m[w * G + hl], f = mw == -INFINITY ? 0.f : exp2f(mw - M);
-      L += f * sm_l[w * G + hl];
-      O += f * sm_o[(w * G + hl) * D + e];
-    }
-    const int64_t bh = (int64_t)b * a.H + g * G + hl;
-    a.out[bh * D + e] = len > 0 ? O / L : 0.f;
-    if (e == 0) {
-      const float z = len > 0 ? M + log2f(L) : -INFINITY;
-      if (a.lse) a.lse[bh] = (float)((double)z * kLn2);
-    }
-  }
-  if (!a.accumulate) return;
-  __syncthreads();
-  for (int64_t j = tid; j < len; j += kPdThreads) {
-    float w = 0.f;
-    for (int hl = 0; hl < G; ++hl) {
-      const float* sl = a.logits + ((int64_t)b * a.H + g * G + hl) * a.max_len;
-      float M = -INFINITY, L = 0.f;
-      for (int x = 0; x < kPdWarps; ++x) M = fmaxf(M, sm_m[x * G + hl]);
-      for (int x = 0; x < kPdWarps; ++x)
-        if (sm_m[x * G + hl] != -INFINITY) L += exp2f(sm_m[x * G + hl] - M) * sm_l[x * G + hl];
-      w += exp2f(sl[j] - M) / L;
-    }
-    c.weights[c.entry(c.page_of(b, j), g, j)] += w;
-  }
+  float* dst = c.weights + c.entry(c.page_of(b, s), g, s);
+  for (int e = 0; e < 4; ++e)
+    if (s + e < n) dst[e] += w[e];
 }
 
 kvc_status check_paged_decode(const Paged& c, int32_t H, int64_t max_len) {
@@ -124,8 +590,53 @@ kvc_status check_paged_decode(const Paged& c, int32_t H, int64_t max_len) {
   return KVC_OK;
 }
 
-size_t paged_decode_ws_bytes(const Paged& c, int32_t H, int64_t max_len, int32_t accumulate) {
-  return kWsAlign + (accumulate ? round_up((size_t)c.batch * H * (size_t)max_len * 4, kWsAlign) : 0);
+int64_t round_unit(int64_t n) { return (n + kPdUnit - 1) / kPdUnit * kPdUnit; }
+
+// CTAs of a call: two per SM, never more than there can be tiles.
+int paged_runs(const Paged& c, int64_t max_len) {
+  const int64_t tiles = (int64_t)c.batch * c.Hkv * ((max_len + kPdTile - 1) / kPdTile);
+  return (int)std::min<int64_t>((int64_t)kPdCtasPerSm * num_sms(), tiles);
+}
+
+// The workspace: counters first (their place depends on the cache alone).
+bool carve(const Paged& c, int H, int64_t max_len, bool accumulate, WsCursor* w, PdArgs* a) {
+  const size_t slots = 2 * (size_t)kPdCtasPerSm * num_sms() * (H / c.Hkv);
+  a->tickets = w->take<uint32_t>((size_t)c.batch * c.Hkv);
+  a->part_ml = w->take<float>(slots * 2);
+  a->part_o = w->take<float>(slots * c.d);
+  if (accumulate) {
+    a->z = w->take<float>((size_t)c.batch * H);
+    a->logits = w->take<float>((size_t)c.batch * H * (size_t)round_unit(max_len));
+  }
+  return w->ok;
+}
+
+template <int D, bool G16>
+kvc_status launch_paged_decode(int runs, cudaStream_t st, const CUtensorMap (&maps)[2], const PdArgs& a) {
+  static ContextCache cache;
+  const kvc_status s = once_per_context(cache, [] {
+    KVC_CUDA_TRY(cudaFuncSetAttribute(paged_decode_kernel<D, G16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)PdSmem<D, G16>::kBytes));
+    return KVC_OK;
+  });
+  if (s != KVC_OK) return s;
+  const Launch l(dim3((unsigned)runs), dim3(kPdThreads), PdSmem<D, G16>::kBytes, st);
+  KVC_CUDA_TRY(l.run(paged_decode_kernel<D, G16>, maps[0], maps[1], a));
+  count_launch();
+  return KVC_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &qr) == cudaSuccess &&
+        qr == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
 }
 
 }  // namespace
@@ -136,12 +647,14 @@ using namespace kvc;
 extern "C" kvc_status kvc_paged_decode_workspace_size(const kvc_paged_cache* c, int32_t num_heads, int64_t max_len,
                                                       int32_t accumulate, size_t* bytes) {
   clear_error();
-  Paged p;
-  kvc_status s = check_paged(c, &p);
-  if (s == KVC_OK) s = check_paged_decode(p, num_heads, max_len);
+  PdArgs a{};
+  kvc_status s = check_paged(c, &a.c);
+  if (s == KVC_OK) s = check_paged_decode(a.c, num_heads, max_len);
   if (s != KVC_OK) return s;
   KVC_CHECK_ARG(bytes != nullptr, "bytes must be non-NULL");
-  *bytes = paged_decode_ws_bytes(p, num_heads, max_len, accumulate);
+  WsCursor w{nullptr, ~size_t(0)};
+  carve(a.c, num_heads, max_len, accumulate != 0, &w, &a);
+  *bytes = w.off;
   return KVC_OK;
 }
 
@@ -160,8 +673,11 @@ extern "C" kvc_status kvc_paged_decode_attention(const kvc_paged_cache* c, const
                 "strides of q must be multiples of 8 elements");
   KVC_CHECK_ARG(scale > 0.f && scale < 1e30f, "scale must be positive and finite");
   KVC_CHECK_ARG(!accumulate || a.c.weights, "accumulating needs the cache's weights");
-  if (!ws || ws_bytes < paged_decode_ws_bytes(a.c, num_heads, max_len, accumulate) || !aligned(ws, kWsAlign))
-    return fail(KVC_ERR_WORKSPACE, "paged decode workspace missing, too small or not 256-B aligned");
+  if (!ws || !aligned(ws, kWsAlign)) return fail(KVC_ERR_WORKSPACE, "paged decode workspace missing or not 256-B aligned");
+  WsCursor w{static_cast<char*>(ws), ws_bytes};
+  if (!carve(a.c, num_heads, max_len, accumulate != 0, &w, &a))
+    return fail(KVC_ERR_WORKSPACE, "paged decode workspace too small");
+  if (!encode_fn()) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   a.q = q;
   a.q_sb = q_stride_b;
   a.q_sh = q_stride_h;
@@ -169,24 +685,34 @@ extern "C" kvc_status kvc_paged_decode_attention(const kvc_paged_cache* c, const
   a.G = num_heads / a.c.Hkv;
   a.c2 = (float)((double)scale * kLog2e);
   a.max_len = max_len;
-  a.accumulate = accumulate != 0;
+  a.ld = round_unit(max_len);
   a.out = out;
   a.lse = lse;
-  a.logits = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsAlign);
   a.err = dev_err;
+  // 4-D maps [page][KV head][slot][d], boxes of 64 columns x 16 slots
+  CUtensorMap maps[2];
+  const uint16_t* srcs[2] = {a.c.k, a.c.v};
   const int d = a.c.d;
-  const size_t smem = (size_t)kPdWarps * a.G * (d + 2) * 4;
-  const Launch l(dim3((unsigned)a.c.Hkv, (unsigned)a.c.batch), dim3(kPdThreads), smem, (cudaStream_t)stream);
-  static ContextCache cache;
-  s = once_per_context(cache, [] {
-    KVC_CUDA_TRY(cudaFuncSetAttribute(paged_decode_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      kPdWarps * kPdMaxG * 130 * 4));
-    KVC_CUDA_TRY(cudaFuncSetAttribute(paged_decode_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      kPdWarps * kPdMaxG * 130 * 4));
-    return KVC_OK;
-  });
-  if (s != KVC_OK) return s;
-  KVC_CUDA_TRY(d == 128 ? l.run(paged_decode_kernel<128>, a) : l.run(paged_decode_kernel<64>, a));
+  for (int i = 0; i < 2; ++i) {
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)a.c.page, (cuuint64_t)a.c.Hkv, (cuuint64_t)a.c.num_pages};
+    cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)a.c.page * d * 2, (cuuint64_t)a.c.page_stride * 2};
+    cuuint32_t box[4] = {64u, (cuuint32_t)kPdUnit, 1u, 1u};
+    cuuint32_t es[4] = {1u, 1u, 1u, 1u};
+    if (encode_fn()(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(srcs[i]), dims, strides, box,
+                    es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled failed for the pages");
+  }
+  const int runs = paged_runs(a.c, max_len);
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (d == 128)
+    s = a.G > 8 ? launch_paged_decode<128, true>(runs, st, maps, a) : launch_paged_decode<128, false>(runs, st, maps, a);
+  else
+    s = a.G > 8 ? launch_paged_decode<64, true>(runs, st, maps, a) : launch_paged_decode<64, false>(runs, st, maps, a);
+  if (s != KVC_OK || !accumulate) return s;
+  const Launch l(dim3((unsigned)((max_len + 4 * kWtThreads - 1) / (4 * kWtThreads)), (unsigned)a.c.Hkv, (unsigned)a.c.batch),
+                 dim3(kWtThreads), 0, st);
+  KVC_CUDA_TRY(l.run(paged_weights_kernel, a));
   count_launch();
   return KVC_OK;
 }
