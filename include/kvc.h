@@ -454,9 +454,10 @@ kvc_status kvc_paged_append_workspace_size(const kvc_paged_cache* c, size_t* byt
  *             (total == batch), a decoding step's
  *  max_seqlen an upper bound of len_b (host value; 1 with cu_seqlens NULL)
  *  scores     [Hkv][total] fp32 contiguous or NULL (read when weights are kept)
- *  ws         kvc_paged_append_workspace_size bytes, 256-B aligned,
- *             ZERO-FILLED before its first use (every call leaves it so); one
- *             call at a time per workspace
+ *  ws         kvc_paged_append_workspace_size bytes, 256-B aligned, the
+ *             first batch * num_kv_heads * 4 bytes (at most) ZERO-FILLED
+ *             before its first use (every call leaves them so); one call at a
+ *             time per workspace
  *  dev_err    KVC_DEV_ERR_SEQLENS: malformed cu_seqlens or len_b >
  *             max_seqlen (nothing of b is appended); KVC_DEV_ERR_PAGES: the
  *             entries do not fit the block table (nothing of b is appended)
@@ -494,8 +495,9 @@ kvc_status kvc_paged_decode_workspace_size(const kvc_paged_cache* c, int32_t num
  *  out      [B][H][d] fp32, contiguous, 16-byte aligned
  *  lse      [B][H] fp32 contiguous, or NULL
  *  ws       kvc_paged_decode_workspace_size(...) bytes, 256-B aligned,
- *           ZERO-FILLED before its first use (every call leaves its counters
- *           so); one call at a time per workspace
+ *           the first batch * num_kv_heads * 4 bytes (at most) ZERO-FILLED
+ *           before its first use (every call leaves them so); one call at a
+ *           time per workspace
  *  dev_err  KVC_DEV_ERR_PAGES: a page id outside the pool or a length
  *           outside [0, max_len] (that sequence: out = 0, lse = -inf, weights
  *           unchanged); KVC_DEV_ERR_TIMEOUT
@@ -530,8 +532,9 @@ kvc_status kvc_paged_evict_workspace_size(const kvc_paged_cache* c, int64_t max_
  *  max_len  upper bound of seq_lens (host value), <= max_pages * page_size
  *  budget   >= 1; recent in [0, budget]
  *  ws       kvc_paged_evict_workspace_size(...) bytes, 256-B aligned,
- *           ZERO-FILLED before its first use (every call leaves its counters
- *           so); one call at a time per workspace
+ *           the first batch * num_kv_heads * 4 bytes (at most) ZERO-FILLED
+ *           before its first use (every call leaves them so); one call at a
+ *           time per workspace
  *  dev_err  KVC_DEV_ERR_PAGES: a page id outside the pool or a length outside
  *           [0, max_len] (nothing of that sequence moves, its length stays)
  * Needs weights, and pos and next_pos when recent > 0; pos moves if kept.

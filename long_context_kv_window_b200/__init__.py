@@ -153,6 +153,8 @@ def _stream(stream: Optional[torch.cuda.Stream], dev: torch.device):
 def _call(dev: torch.device, fn, *args) -> int:
     """Run one libkvc entry point with `dev` current (kernel launches and the
     per-device function attributes refer to the current device)."""
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args)
     with torch.cuda.device(dev):
         return fn(*args)
 
@@ -590,11 +592,17 @@ def prefill_varlen_workspace_size(H: int, Hkv: int, d: int, batch: int, total_q:
     return int(out.value)
 
 
-def _launch_stream(stream: Optional[torch.cuda.Stream], dev: torch.device) -> torch.cuda.Stream:
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    if s.device != dev:
-        raise ValueError(f"stream is on {s.device}, the tensors on {dev}")
-    return s
+def _adr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream: Optional[torch.cuda.Stream], dev: torch.device) -> int:
+    """_stream as a plain handle, without the stream object of the current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream
 
 
 def _scratch(nbytes: int, dev: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
@@ -651,10 +659,10 @@ def kvc_prefill_attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     if ws is None:
         ws = _scratch(prefill_varlen_workspace_size(H, Hkv, d, B, total_q, max_seqlen_q, max_seqlen_k), dev, stream)
     sc = float(1.0 / math.sqrt(d) if scale is None else scale)
-    _check(_call(dev, lib().kvc_prefill_attention_varlen, _ptr(q), q.stride(0), q.stride(1), _ptr(k), k.stride(0),
-                 k.stride(1), _ptr(v), v.stride(0), v.stride(1), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, total_q,
-                 total_k, int(max_seqlen_q), int(max_seqlen_k), H, Hkv, d, sc, _ptr(out), _ptr(lse), _ptr(ws),
-                 _ws_bytes(ws, dev), _ptr(dev_err), _stream(stream, dev)), "kvc_prefill_attention_varlen")
+    _check(_call(dev, lib().kvc_prefill_attention_varlen, _adr(q), q.stride(0), q.stride(1), _adr(k), k.stride(0),
+                 k.stride(1), _adr(v), v.stride(0), v.stride(1), _adr(cu_seqlens_q), _adr(cu_seqlens_k), B, total_q,
+                 total_k, int(max_seqlen_q), int(max_seqlen_k), H, Hkv, d, sc, _adr(out), _adr(lse), _adr(ws),
+                 _ws_bytes(ws, dev), _adr(dev_err), _raw_stream(stream, dev)), "kvc_prefill_attention_varlen")
     _used_on(stream, made_out, made_lse)
     return out, lse
 
@@ -727,10 +735,10 @@ class PagedCache:
                    pos=torch.zeros(shape, dtype=i32, device=device),
                    next_pos=torch.zeros(batch, dtype=i32, device=device))
 
-    def _workspace(self, call: str, size_args: tuple, stream: torch.cuda.Stream) -> torch.Tensor:
-        """A workspace of `call`, zero-filled once, on the stream that uses it.
-        The counters that have to start at zero come first and depend on the
-        cache alone, so a workspace serves every call that needs no more."""
+    def _workspace(self, call: str, size_args: tuple, handle: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+        """A workspace of `call` on the stream of that handle.  Its counters,
+        which start at zero and come first, depend on the cache alone, so a
+        workspace serves every call that needs no more bytes."""
         need = self._need.get((call, size_args))
         if need is None:
             out = ctypes.c_size_t(0)
@@ -738,12 +746,13 @@ class PagedCache:
                    call + "_workspace_size")
             need = self._need[call, size_args] = max(int(out.value), 1)
         capturing = torch.cuda.is_current_stream_capturing()
-        ws = None if capturing else self._ws.get((call, stream.cuda_stream))
+        ws = None if capturing else self._ws.get((call, handle))
         if ws is None or ws.numel() < need:
-            with torch.cuda.stream(stream):
-                ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            with torch.cuda.stream(stream):  # None: the current stream
+                ws = _workspace(need, self.device)
+                ws[:4 * self.batch * self.num_kv_heads].zero_()
             if not capturing:
-                self._ws[call, stream.cuda_stream] = ws
+                self._ws[call, handle] = ws
         return ws
 
     def _max_len(self, max_len: Optional[int]) -> int:
@@ -783,12 +792,12 @@ def kvc_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seq
     if scores is not None:
         _dense(scores, "scores", (Hkv, total), torch.float32, dev)
     _err_word(dev_err, dev)
-    st = _launch_stream(stream, dev)
+    st = _raw_stream(stream, dev)
     if ws is None:
-        ws = cache._workspace("kvc_paged_append", (), st)
-    _check(_call(dev, lib().kvc_paged_append, cache._ref, _ptr(k), _ptr(v), k.stride(0), k.stride(1),
-                 _ptr(cu_seqlens), total, int(max_seqlen), _ptr(idx), kk, _ptr(scores), _ptr(ws), _ws_bytes(ws, dev),
-                 _ptr(dev_err), _stream(st, dev)), "kvc_paged_append")
+        ws = cache._workspace("kvc_paged_append", (), st, stream)
+    _check(_call(dev, lib().kvc_paged_append, cache._ref, _adr(k), _adr(v), k.stride(0), k.stride(1),
+                 _adr(cu_seqlens), total, int(max_seqlen), _adr(idx), kk, _adr(scores), _adr(ws), _ws_bytes(ws, dev),
+                 _adr(dev_err), st), "kvc_paged_append")
     return cache
 
 
@@ -818,13 +827,13 @@ def kvc_paged_decode_attention(q: torch.Tensor, cache: PagedCache, scale: Option
     _dense(lse, "lse", (B, H), torch.float32, dev)
     _err_word(dev_err, dev)
     max_len = cache._max_len(max_len)
-    st = _launch_stream(stream, dev)
+    st = _raw_stream(stream, dev)
     if ws is None:
-        ws = cache._workspace("kvc_paged_decode", (H, max_len, int(accumulate)), st)
+        ws = cache._workspace("kvc_paged_decode", (H, max_len, int(accumulate)), st, stream)
     sc = float(1.0 / math.sqrt(d) if scale is None else scale)
-    _check(_call(dev, lib().kvc_paged_decode_attention, cache._ref, _ptr(q), q.stride(0), q.stride(1), H, sc, max_len,
-                 int(accumulate), _ptr(out), _ptr(lse), _ptr(ws), _ws_bytes(ws, dev), _ptr(dev_err),
-                 _stream(st, dev)), "kvc_paged_decode_attention")
+    _check(_call(dev, lib().kvc_paged_decode_attention, cache._ref, _adr(q), q.stride(0), q.stride(1), H, sc, max_len,
+                 int(accumulate), _adr(out), _adr(lse), _adr(ws), _ws_bytes(ws, dev), _adr(dev_err), st),
+           "kvc_paged_decode_attention")
     _used_on(stream, made_out, made_lse)
     return out, lse
 
@@ -842,11 +851,11 @@ def kvc_paged_evict(cache: PagedCache, budget: int, recent: int, max_len: Option
         raise ValueError("keeping recent entries needs a cache with pos and next_pos")
     _err_word(dev_err, dev)
     max_len = cache._max_len(max_len)
-    st = _launch_stream(stream, dev)
+    st = _raw_stream(stream, dev)
     if ws is None:
-        ws = cache._workspace("kvc_paged_evict", (max_len, int(budget)), st)
-    _check(_call(dev, lib().kvc_paged_evict, cache._ref, max_len, int(budget), int(recent), _ptr(ws),
-                 _ws_bytes(ws, dev), _ptr(dev_err), _stream(st, dev)), "kvc_paged_evict")
+        ws = cache._workspace("kvc_paged_evict", (max_len, int(budget)), st, stream)
+    _check(_call(dev, lib().kvc_paged_evict, cache._ref, max_len, int(budget), int(recent), _adr(ws),
+                 _ws_bytes(ws, dev), _adr(dev_err), st), "kvc_paged_evict")
     return cache
 
 

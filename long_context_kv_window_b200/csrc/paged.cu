@@ -20,7 +20,7 @@ namespace {
 // first store.  Lengths move on once every CTA has read them: the last CTA of
 // the grid (a ticket counter, returned to zero) adds the new entries.
 constexpr int kAppThreads = 256;
-constexpr int kAppRows = 16;
+constexpr int kAppRows = 8;
 constexpr int kAppUnroll = 4;
 
 struct AppArgs {
@@ -55,7 +55,7 @@ __device__ AppSeq app_seq(const AppArgs& a, int b) {
   return s;
 }
 
-__global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a) {
+__global__ void __launch_bounds__(kAppThreads, 4) append_kernel(const AppArgs a) {
   __shared__ int last;
   pdl_wait();
   const int b = blockIdx.y;
@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a) {
   const AppSeq q = app_seq(a, b);
   const int64_t r0 = (int64_t)blockIdx.x * kAppRows;
   const int rows = (int)(q.kept - r0 < kAppRows ? q.kept - r0 : kAppRows);  // <= 0 past the entries
-  const int np = c.d / 8;                                                 // 16-byte pieces per row
-  const int per_row = np * c.Hkv, items = rows * per_row;
+  const int log_np = c.d == 128 ? 4 : 3, np = 1 << log_np;                // 16-byte pieces per row
+  const int items = rows * np * c.Hkv;
   const int64_t npos = c.next_pos ? c.next_pos[b] : 0;
   for (int i0 = threadIdx.x; i0 < items; i0 += kAppThreads * kAppUnroll) {
     uint4 kv[kAppUnroll], vv[kAppUnroll];
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a) {
       const int i = i0 + u * kAppThreads;
       dst[u] = -1;
       if (i >= items) continue;
-      const int r = i / per_row, g = (i % per_row) / np, piece = i % np;
+      const int piece = i & (np - 1), r = (i >> log_np) / c.Hkv, g = (i >> log_np) % c.Hkv;
       const int64_t slot = q.slot + r0 + r;
       int64_t t = r0 + r;  // local token
       if (a.idx) {
@@ -127,21 +127,35 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a) {
 
 // -------------------------------------------------------------------- evict
 // CTA (KV head, sequence).  Keys are the order-preserving uint32 image of the
-// weights (recent entries the largest key, NaN 0); a radix select finds the
-// key T of the budget-th largest; one pass in slot order ranks the keys equal
-// to T and lists the slots given up below the budget and the kept slots above
-// it; their rows are then moved pairwise.  Sources lie at or above the budget
-// and destinations below it, so the moves need no order among themselves.
-constexpr int kEvThreads = 1024;
+// weights (recent entries the largest key, NaN 0), kept in shared memory where
+// they fit.  One entry too many -- every decoding step -- needs the lowest
+// ranked entry only, one reduction.  Otherwise the budget-th largest key T is
+// found by histograms of 2048 equal bins over the range of the keys, then over
+// the bin that holds it, until the bin is one key or is kept whole (weights
+// span few exponents, so bins over their range part them better than fixed
+// digits do).  Warps then own runs of slots: counted with ballots, prefixed
+// once over the warps, listed with ballots: the slots given up below the
+// budget and the kept slots above it, both ascending.
+// The rows are moved pairwise; sources lie at or above the budget and
+// destinations below it, so the moves need no order among themselves.  Few
+// moves are made by the CTA itself, many by a second kernel over all SMs.
 constexpr uint32_t kRecentKey = 0xFFFFFFFFu;
+constexpr int kEvBins = 2048;
+constexpr int64_t kEvSmemKeys = 48 * 1024;  // keys of a pair held in shared memory (192 KB)
+constexpr int64_t kEvInline = 32;           // moves a pair's CTA makes itself
+constexpr int64_t kEvSmall = 4096;          // up to here a pair is a CTA of 256 threads, else of 1024
+constexpr int kMvThreads = 256;
+constexpr int kMvRows = 32;                 // moves per CTA of the second kernel and round
 
 struct EvArgs {
   Paged c;
   int64_t max_len, budget, recent;
   int64_t max_move;
   uint32_t* tickets;  // [batch]
-  uint32_t* keys;     // [batch*Hkv][max_len]
-  int32_t* moves;     // [batch*Hkv][2][max_move]: slots given up, kept slots above the budget
+  int32_t* moves;     // [batch*Hkv]: moves of the pair
+  int32_t* lists;     // [batch*Hkv][2][max_move]: slots given up, kept slots above the budget
+  uint32_t* keys;     // [batch*Hkv][max_len], or nullptr: shared memory
+  int in_place;       // the CTA makes the moves itself
   int32_t* err;
 };
 
@@ -151,130 +165,231 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix of `v` over the CTA's threads, and the total.
-__device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
+// Moves i0, i0 + step, ... of a pair's list: 16-byte pieces, weight, position.
+__device__ __forceinline__ void move_rows(const Paged& c, int b, int g, const int32_t* give, const int32_t* take, int i0,
+                                          int i1, int tid, int threads) {
+  const int np = c.d / 8;
+#pragma unroll 4
+  for (int i = i0 * np + tid; i < i1 * np; i += threads) {
+    const int m = i / np, piece = i % np;
+    const int64_t from = take[m], to = give[m];
+    const int pf = c.page_of(b, from), pt = c.page_of(b, to);
+    const int64_t src = c.row(pf, g, from) + piece * 8, dst = c.row(pt, g, to) + piece * 8;
+    const uint4 kv = *reinterpret_cast<const uint4*>(c.k + src), vv = *reinterpret_cast<const uint4*>(c.v + src);
+    *reinterpret_cast<uint4*>(c.k + dst) = kv;
+    *reinterpret_cast<uint4*>(c.v + dst) = vv;
+    if (piece == 0) {
+      const int64_t ef = c.entry(pf, g, from), et = c.entry(pt, g, to);
+      c.weights[et] = c.weights[ef];
+      if (c.pos) c.pos[et] = c.pos[ef];
     }
-    warp_sums[lane] = s;
   }
-  __syncthreads();
-  const int before = warp == 0 ? 0 : warp_sums[warp - 1];
-  *total = warp_sums[31];
-  __syncthreads();
-  return before + x - v;
 }
 
-__global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvArgs a) {
-  __shared__ uint32_t hist[2048];
-  __shared__ int warp_sums[32];
-  __shared__ int bad, sh_bin, sh_left;
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kPer = kEvBins / kThreads;  // bins per thread
+  extern __shared__ uint32_t sm_keys[];
+  __shared__ uint32_t hist[kEvBins];
+  __shared__ uint32_t red[3][kWarps];
+  __shared__ int cnt[2][kWarps];
+  __shared__ int bad, sh_bin, sh_left, sh_in;
   pdl_wait();
   const Paged& c = a.c;
-  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  const int64_t n = c.seq_lens[b];
+  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = c.seq_lens[b], budget = (int)std::min<int64_t>(a.budget, 0x7FFFFFFF);
+  const int64_t pair = (int64_t)b * c.Hkv + g;
+  int32_t* give = a.lists + pair * 2 * a.max_move;
+  int32_t* take = give + a.max_move;
   if (tid == 0) bad = n < 0 || n > a.max_len;
   __syncthreads();
-  if (!bad)
-    for (int64_t s = (int64_t)tid * c.page; s < n; s += (int64_t)kEvThreads * c.page)
-      if (c.page_of(b, s) < 0) bad = 1;
-  __syncthreads();
-  if (bad) {
-    if (tid == 0) set_dev_err(a.err, KVC_DEV_ERR_PAGES);
-  } else if (n > a.budget) {
+  int n_moves = 0;
+  if (!bad && n > budget) {
+    // ---- the keys, and the lowest ranked entry: lowest key, then highest slot
+    uint32_t* keys = a.keys ? a.keys + pair * a.max_len : sm_keys;
     const int64_t limit = a.recent > 0 ? (int64_t)c.next_pos[b] - a.recent : 0;
-    uint32_t* keys = a.keys + ((int64_t)b * c.Hkv + g) * a.max_len;
-    for (int64_t s = tid; s < n; s += kEvThreads) {
-      const int64_t e = c.entry(c.page_of(b, s), g, s);
-      keys[s] = a.recent > 0 && c.pos[e] >= limit ? kRecentKey : weight_key(c.weights[e]);
-    }
-    // the budget-th largest key, 11 + 11 + 10 bits from the top
-    uint32_t prefix = 0, mask = 0;
-    int left = (int)a.budget;  // kept keys that match the prefix so far
-    for (int level = 0; level < 3; ++level) {
-      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bins = level == 2 ? 1024 : 2048;
-      for (int i = tid; i < 2048; i += kEvThreads) hist[i] = 0u;
-      __syncthreads();
-      for (int64_t s = tid; s < n; s += kEvThreads) {
-        const uint32_t key = keys[s];
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
+    const bool one = n - budget == 1;
+    uint32_t lo = kRecentKey, hi = 0u;
+    int low_slot = -1, fresh = 0, gone = 0;
+#pragma unroll 4
+    for (int s = tid; s < n; s += kThreads) {
+      const int p = c.page_of(b, s);
+      uint32_t key = 0u;
+      if (p < 0) {
+        gone = 1;
+      } else {
+        const int64_t e = c.entry(p, g, s);
+        key = weight_key(c.weights[e]);
+        if (a.recent > 0 && c.pos[e] >= limit) key = kRecentKey;
       }
-      __syncthreads();
-      // thread t holds two bins from the top: 2t and 2t + 1 counted from the largest
-      const int h0 = 2 * tid < bins ? (int)hist[bins - 1 - 2 * tid] : 0;
-      const int h1 = 2 * tid + 1 < bins ? (int)hist[bins - 2 - 2 * tid] : 0;
-      int total;
-      const int above = block_prefix(h0 + h1, warp_sums, &total);
-      if (above < left && left <= above + h0) {
-        sh_bin = bins - 1 - 2 * tid;
-        sh_left = left - above;
-      } else if (above + h0 < left && left <= above + h0 + h1) {
-        sh_bin = bins - 2 - 2 * tid;
-        sh_left = left - above - h0;
+      if (!one) keys[s] = key;
+      if (key <= lo) {
+        lo = key;
+        low_slot = s;
       }
-      __syncthreads();
-      prefix |= (uint32_t)sh_bin << shift;
-      mask |= (uint32_t)(bins - 1) << shift;
-      left = sh_left;
-      __syncthreads();
+      if (key == kRecentKey) ++fresh; else hi = max(hi, key);
     }
-    const uint32_t T = prefix;  // `left` of the keys equal to T are kept, the lowest slots
-    int32_t* give = a.moves + ((int64_t)b * c.Hkv + g) * 2 * a.max_move;
-    int32_t* take = give + a.max_move;
-    int eq_seen = 0, n_give = 0, n_take = 0;
-    for (int64_t s0 = 0; s0 < n; s0 += kEvThreads) {
-      const int64_t s = s0 + tid;
-      const uint32_t key = s < n ? keys[s] : 0u;
-      const int eq = s < n && key == T;
-      int total;
-      const int rank = eq_seen + block_prefix(eq, warp_sums, &total);
-      eq_seen += total;
-      const bool kept = s < n && (key > T || (eq && rank < left));
-      const int gv = s < n && s < a.budget && !kept, tk = s >= a.budget && kept;
-      const int both = block_prefix(gv | (tk << 16), warp_sums, &total);
-      if (gv) give[n_give + (both & 0xFFFF)] = (int32_t)s;
-      if (tk) take[n_take + (both >> 16)] = (int32_t)s;
-      n_give += total & 0xFFFF;
-      n_take += total >> 16;
+    if (gone) bad = 1;
+    {
+      const uint32_t lo_w = __reduce_min_sync(0xffffffffu, lo);
+      const int slot_w = __reduce_max_sync(0xffffffffu, lo == lo_w ? low_slot : -1);
+      const uint32_t hi_w = __reduce_max_sync(0xffffffffu, hi);
+      const int fresh_w = __reduce_add_sync(0xffffffffu, fresh);
+      if (lane == 0) {
+        red[0][warp] = lo_w;
+        red[1][warp] = (uint32_t)slot_w;
+        red[2][warp] = hi_w;
+        cnt[0][warp] = fresh_w;
+      }
     }
     __syncthreads();
-    const int np = c.d / 8;
-    for (int i = tid; i < n_take * np; i += kEvThreads) {
-      const int m = i / np, piece = i % np;
-      const int64_t from = take[m], to = give[m];
-      const int pf = c.page_of(b, from), pt = c.page_of(b, to);
-      const int64_t src = c.row(pf, g, from) + piece * 8, dst = c.row(pt, g, to) + piece * 8;
-      *reinterpret_cast<uint4*>(c.k + dst) = *reinterpret_cast<const uint4*>(c.k + src);
-      *reinterpret_cast<uint4*>(c.v + dst) = *reinterpret_cast<const uint4*>(c.v + src);
-      if (piece == 0) {
-        const int64_t ef = c.entry(pf, g, from), et = c.entry(pt, g, to);
-        c.weights[et] = c.weights[ef];
-        if (c.pos) c.pos[et] = c.pos[ef];
+    lo = red[0][0];
+    hi = red[2][0];
+    fresh = cnt[0][0];
+    low_slot = (int)red[1][0];
+    for (int w = 1; w < kWarps; ++w) {
+      if (red[0][w] < lo || (red[0][w] == lo && (int)red[1][w] > low_slot)) low_slot = (int)red[1][w];
+      lo = min(lo, red[0][w]);
+      hi = max(hi, red[2][w]);
+      fresh += cnt[0][w];
+    }
+    __syncthreads();
+    if (!bad && one) {
+      if (low_slot < budget) {
+        if (tid == 0) {
+          give[0] = low_slot;
+          take[0] = budget;
+        }
+        n_moves = 1;
+      }
+    } else if (!bad) {
+      // ---- T: `left` of the keys equal to T are kept, the lowest slots
+      uint32_t T = kRecentKey;
+      int left = budget;
+      if (fresh < budget) {
+        left = budget - fresh;
+        for (;;) {
+          T = lo;
+          if (lo == hi) break;
+          const int bits = 32 - __clz(hi - lo), sh = bits > 11 ? bits - 11 : 0;
+          for (int i = tid; i < kEvBins; i += kThreads) hist[i] = 0u;
+          __syncthreads();
+#pragma unroll 4
+          for (int s = tid; s < n; s += kThreads) {
+            const uint32_t key = keys[s];
+            if (key >= lo && key <= hi) atomicAdd(&hist[(key - lo) >> sh], 1u);
+          }
+          __syncthreads();
+          int h[kPer], sum = 0;  // this thread's bins, from the largest down
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            h[u] = (int)hist[kEvBins - 1 - kPer * tid - u];
+            sum += h[u];
+          }
+          int inc = sum;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+          }
+          if (lane == 31) cnt[0][warp] = inc;
+          __syncthreads();
+          int above = inc - sum;
+          for (int w = 0; w < warp; ++w) above += cnt[0][w];
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            if (above < left && left <= above + h[u]) {
+              sh_bin = kEvBins - 1 - kPer * tid - u;
+              sh_left = left - above;
+              sh_in = h[u];
+            }
+            above += h[u];
+          }
+          __syncthreads();
+          left = sh_left;
+          lo += (uint32_t)sh_bin << sh;
+          hi = min(hi, lo + ((1u << sh) - 1u));
+          T = lo;
+          const bool whole = sh_in == left;
+          __syncthreads();
+          if (whole) {  // every key of the bin is kept
+            left = n;
+            break;
+          }
+          if (sh == 0) break;
+        }
+      }
+      // ---- ranks and lists; warp w owns the slots [w * run, (w + 1) * run)
+      const int run = (n + kThreads - 1) / kThreads * 32, s_end = min(n, (warp + 1) * run);
+      int eq = 0;
+      for (int s = warp * run + lane; s < s_end; s += 32) eq += keys[s] == T;
+      eq = __reduce_add_sync(0xffffffffu, eq);
+      if (lane == 0) cnt[0][warp] = eq;
+      __syncthreads();
+      int eq_before = 0;
+      for (int w = 0; w < warp; ++w) eq_before += cnt[0][w];
+      __syncthreads();
+      int at[2] = {0, 0};  // slots given up and slots taken before this warp's
+      for (int phase = 0; phase < 2; ++phase) {
+        int rank = eq_before, n_give = at[0], n_take = at[1];
+        const unsigned below = (1u << lane) - 1u;
+        for (int s0 = warp * run; s0 < s_end; s0 += 32) {
+          const int s = s0 + lane;
+          const bool in = s < s_end;
+          const uint32_t key = in ? keys[s] : 0u;
+          const unsigned eqs = __ballot_sync(0xffffffffu, in && key == T);
+          const bool kept = in && (key > T || (key == T && rank + __popc(eqs & below) < left));
+          const unsigned gv = __ballot_sync(0xffffffffu, in && s < budget && !kept);
+          const unsigned tk = __ballot_sync(0xffffffffu, s >= budget && kept);
+          if (phase == 1) {
+            if ((gv >> lane) & 1) give[n_give + __popc(gv & below)] = s;
+            if ((tk >> lane) & 1) take[n_take + __popc(tk & below)] = s;
+          }
+          rank += __popc(eqs);
+          n_give += __popc(gv);
+          n_take += __popc(tk);
+        }
+        if (phase == 0) {
+          if (lane == 0) {
+            cnt[0][warp] = n_give;
+            cnt[1][warp] = n_take;
+          }
+          __syncthreads();
+          for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) {
+              at[0] += cnt[0][w];
+              at[1] += cnt[1][w];
+            }
+            n_moves += cnt[1][w];
+          }
+        }
       }
     }
+    __syncthreads();
+    if (a.in_place && n_moves > 0) move_rows(c, b, g, give, take, 0, n_moves, tid, kThreads);
   }
-  // the length of the sequence moves once all its heads have read it
-  __syncthreads();
   if (tid == 0) {
+    if (bad) set_dev_err(a.err, KVC_DEV_ERR_PAGES);
+    a.moves[pair] = n_moves;
+    // the length of the sequence moves once all its heads have read it
     __threadfence();
     if (atomicAdd(&a.tickets[b], 1u) == (uint32_t)c.Hkv - 1) {
-      if (!bad && n > a.budget) c.seq_lens[b] = (int32_t)a.budget;
+      if (!bad && n > budget) c.seq_lens[b] = budget;
       a.tickets[b] = 0u;
     }
   }
+}
+
+// CTA (round of moves, KV head, sequence)
+__global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvArgs a) {
+  pdl_wait();
+  const int g = blockIdx.y, b = blockIdx.z;
+  const int64_t pair = (int64_t)b * a.c.Hkv + g;
+  const int n = a.moves[pair];
+  const int32_t* give = a.lists + pair * 2 * a.max_move;
+  const int i0 = (int)blockIdx.x * kMvRows;
+  if (i0 < n) move_rows(a.c, b, g, give, give + a.max_move, i0, min(n, i0 + kMvRows), threadIdx.x, kMvThreads);
 }
 
 int64_t evict_max_move(int64_t max_len, int64_t budget) {
@@ -287,10 +402,31 @@ kvc_status check_evict(const Paged& c, int64_t max_len, int64_t budget) {
   return KVC_OK;
 }
 
-size_t evict_ws_bytes(const Paged& c, int64_t max_len, int64_t budget) {
+// The workspace: counters first (their place depends on the cache alone).
+bool carve_evict(const Paged& c, int64_t max_len, int64_t budget, WsCursor* w, EvArgs* a) {
   const size_t bg = (size_t)c.batch * c.Hkv;
-  return round_up((size_t)c.batch * 4, kWsAlign) + round_up(bg * (size_t)max_len * 4, kWsAlign) +
-         round_up(bg * 2 * (size_t)std::max<int64_t>(1, evict_max_move(max_len, budget)) * 4, kWsAlign);
+  a->max_move = std::max<int64_t>(1, evict_max_move(max_len, budget));
+  a->tickets = w->take<uint32_t>((size_t)c.batch);
+  a->moves = w->take<int32_t>(bg);
+  a->lists = w->take<int32_t>(bg * 2 * (size_t)a->max_move);
+  a->keys = max_len > kEvSmemKeys ? w->take<uint32_t>(bg * (size_t)max_len) : nullptr;
+  return w->ok;
+}
+
+template <int kThreads>
+kvc_status launch_evict(const EvArgs& a, cudaStream_t st) {
+  static ContextCache cache;
+  const kvc_status s = once_per_context(cache, [] {
+    KVC_CUDA_TRY(cudaFuncSetAttribute(evict_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)kEvSmemKeys * 4));
+    return KVC_OK;
+  });
+  if (s != KVC_OK) return s;
+  const size_t smem = a.keys ? 0 : (size_t)a.max_len * 4;
+  const Launch l(dim3((unsigned)a.c.Hkv, (unsigned)a.c.batch), dim3(kThreads), smem, st);
+  KVC_CUDA_TRY(l.run(evict_kernel<kThreads>, a));
+  count_launch();
+  return KVC_OK;
 }
 
 }  // namespace
@@ -354,7 +490,10 @@ extern "C" kvc_status kvc_paged_evict_workspace_size(const kvc_paged_cache* c, i
   if (s == KVC_OK) s = check_evict(p, max_len, budget);
   if (s != KVC_OK) return s;
   KVC_CHECK_ARG(bytes != nullptr, "bytes must be non-NULL");
-  *bytes = evict_ws_bytes(p, max_len, budget);
+  WsCursor w{nullptr, ~size_t(0)};
+  EvArgs a{};
+  carve_evict(p, max_len, budget, &w, &a);
+  *bytes = w.off;
   return KVC_OK;
 }
 
@@ -369,21 +508,20 @@ extern "C" kvc_status kvc_paged_evict(const kvc_paged_cache* c, int64_t max_len,
   KVC_CHECK_ARG(recent >= 0 && recent <= budget, "need 0 <= recent <= budget");
   KVC_CHECK_ARG(a.c.weights, "eviction ranks by the cache's weights: they must be non-NULL");
   KVC_CHECK_ARG(recent == 0 || a.c.pos, "keeping recent entries needs pos and next_pos");
-  if (!ws || ws_bytes < evict_ws_bytes(a.c, max_len, budget) || !aligned(ws, kWsAlign))
-    return fail(KVC_ERR_WORKSPACE, "evict workspace missing, too small or not 256-B aligned");
-  const size_t bg = (size_t)a.c.batch * a.c.Hkv;
+  if (!ws || !aligned(ws, kWsAlign)) return fail(KVC_ERR_WORKSPACE, "evict workspace missing or not 256-B aligned");
+  WsCursor w{static_cast<char*>(ws), ws_bytes};
+  if (!carve_evict(a.c, max_len, budget, &w, &a)) return fail(KVC_ERR_WORKSPACE, "evict workspace too small");
   a.max_len = max_len;
   a.budget = budget;
   a.recent = recent;
-  a.max_move = std::max<int64_t>(1, evict_max_move(max_len, budget));
-  WsCursor wc{static_cast<char*>(ws), ws_bytes};
-  a.tickets = wc.take<uint32_t>((size_t)a.c.batch);
-  a.keys = wc.take<uint32_t>(bg * (size_t)max_len);
-  a.moves = wc.take<int32_t>(bg * 2 * (size_t)a.max_move);
-  if (!wc.ok) return fail(KVC_ERR_WORKSPACE, "evict workspace too small");
+  a.in_place = a.max_move <= kEvInline;
   a.err = dev_err;
-  const Launch l(dim3((unsigned)a.c.Hkv, (unsigned)a.c.batch), dim3(kEvThreads), 0, (cudaStream_t)stream);
-  KVC_CUDA_TRY(l.run(evict_kernel, a));
+  const cudaStream_t st = (cudaStream_t)stream;
+  s = max_len <= kEvSmall ? launch_evict<256>(a, st) : launch_evict<1024>(a, st);
+  if (s != KVC_OK || a.in_place) return s;
+  const Launch l(dim3((unsigned)((a.max_move + kMvRows - 1) / kMvRows), (unsigned)a.c.Hkv, (unsigned)a.c.batch),
+                 dim3(kMvThreads), 0, st);
+  KVC_CUDA_TRY(l.run(evict_move_kernel, a));
   count_launch();
   return KVC_OK;
 }

@@ -50,6 +50,11 @@ constexpr int kPdTile = kPdUnit * kPdWarps;  // entries of a tile
 constexpr int kPdMaxG = 16;
 constexpr int kPdCtasPerSm = 2;
 constexpr int kPdMaxBatch = 1024;
+// What a pair costs beside its tiles, in tiles: reading q, joining the warps,
+// writing the result.  A ragged batch of 64 (1..8192 entries, 32/8 heads, half
+// of them within one tile) took 111 us with 0, 64.6 with 2, 58.3 with 3, 56.6
+// with 4, 56.1 with 6; batches of equal lengths do not care.
+constexpr int kPdPairCost = 4;
 constexpr float kPdSlack = 8.f;
 constexpr double kLog2e = 1.4426950408889634;
 constexpr double kLn2 = 0.6931471805599453;
@@ -122,21 +127,28 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint3
   lo = pack_bf16(x - f.x, y - f.y);
 }
 
-// The runs: pair p = (b, g) holds tiles [first(p), first(p) + nu(b)) of the
-// row of all tiles; run i holds [total * i / runs, total * (i + 1) / runs).
+// Tiles of a sequence of n entries, per KV head.
+__device__ __forceinline__ int pd_tiles(int n, int64_t max_len) {
+  return n > 0 && n <= max_len ? (n + kPdTile - 1) / kPdTile : 0;
+}
+// The runs: a pair of nu tiles is kPdPairCost + nu places of one row (what it
+// costs to begin and end a pair, then its tiles); run i holds the places
+// [total * i / runs, total * (i + 1) / runs).
 struct Runs {
   int64_t total;
   int runs;
   __device__ __forceinline__ int64_t start(int i) const { return total * i / runs; }
-  // the run that holds tile x
+  // the run that holds place x
   __device__ __forceinline__ int of(int64_t x) const { return (int)(((x + 1) * runs + total - 1) / total) - 1; }
 };
 
-// A piece of a pair inside a run.
+// A pair's places inside a run.
 struct Piece {
   int b, g;
-  int len, nu;  // entries and tiles of the pair
-  int t0, t1;   // tiles of the piece
+  int len, nu;   // entries and tiles of the pair
+  int t0, t1;    // tiles of the piece (none if t1 <= t0)
+  int64_t pair;  // the pair's first tile, as a place
+  int64_t next;  // the place behind the piece
 };
 
 template <int D, bool G16>
@@ -147,7 +159,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* merge = reinterpret_cast<float*>(sm + L::kRing);                       // [2][kRows][D + 4]
-  int* first = reinterpret_cast<int*>(sm + L::kRing + L::kMerge);              // [B + 1]: tiles before sequence b (per head)
+  int* first = reinterpret_cast<int*>(sm + L::kRing + L::kMerge);              // [B + 1]: places before sequence b (per head)
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kRing + L::kMerge + (kPdMaxBatch + 2) / 2 * 8);  // [warps][stages]
   int* flags = reinterpret_cast<int*>(full + kPdWarps * L::kStages);           // abort, last, warp totals, warps' bad flags
   volatile int* abort_flag = flags;
@@ -163,15 +175,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     tc::prefetch_tmap(&vmap);
   }
   pdl_wait();  // the cache and q may come from the previous kernels of the stream
-  // ---- tiles before each sequence
+  pdl_trigger();  // this grid is resident at once: the next kernel may be brought in as its CTAs leave
+  // ---- places before each sequence
   {
     const int per = (B + kPdThreads - 1) / kPdThreads, b0 = tid * per;
     int mine = 0;
     for (int u = 0; u < per; ++u) {
       const int b = b0 + u;
       if (b >= B) break;
-      const int n = c.seq_lens[b];
-      mine += n > 0 && n <= a.max_len ? (n + kPdTile - 1) / kPdTile : 0;
+      const int nu = pd_tiles(c.seq_lens[b], a.max_len);
+      mine += nu > 0 ? nu + kPdPairCost : 0;
     }
     int inc = mine;
 #pragma unroll
@@ -187,8 +200,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       const int b = b0 + u;
       if (b >= B) break;
       first[b] = at;
-      const int n = c.seq_lens[b];
-      at += n > 0 && n <= a.max_len ? (n + kPdTile - 1) / kPdTile : 0;
+      const int nu = pd_tiles(c.seq_lens[b], a.max_len);
+      at += nu > 0 ? nu + kPdPairCost : 0;
       if (b == B - 1) first[B] = at;
     }
     __syncthreads();
@@ -210,21 +223,25 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   if (run >= rs.runs) return;
   const int64_t x0 = rs.start(run), x1 = rs.start(run + 1);
 
-  // the piece of the run [x, x1) that starts at x
+  // the piece of the run [x0, x1) that starts at place x
   auto piece_at = [&](int64_t x) {
     Piece p;
-    int lo = 0, hi = B - 1;  // the last sequence whose tiles begin at or before x
+    int lo = 0, hi = B - 1;  // the last sequence whose places begin at or before x
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if ((int64_t)first[mid] * Hkv <= x) lo = mid; else hi = mid - 1;
     }
-    p.b = lo;
-    p.nu = first[lo + 1] - first[lo];
+    const int places = first[lo + 1] - first[lo];
     const int64_t r = x - (int64_t)first[lo] * Hkv;
-    p.g = (int)(r / p.nu);
-    p.t0 = (int)(r % p.nu);
-    p.t1 = (int)std::min<int64_t>(p.nu, p.t0 + (x1 - x));
-    p.len = c.seq_lens[p.b];
+    const int at = (int)(r % places);
+    p.b = lo;
+    p.g = (int)(r / places);
+    p.nu = places - kPdPairCost;
+    p.pair = x - at + kPdPairCost;
+    p.next = std::min<int64_t>(x1, x - at + places);
+    p.t0 = max(0, at - kPdPairCost);
+    p.t1 = (int)(p.next - p.pair);
+    p.len = c.seq_lens[lo];
     return p;
   };
 
@@ -233,7 +250,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   const uint32_t ring_u32 = tc::smem_u32(ring);
   uint64_t* bar = full + warp * L::kStages;
   Piece pp = piece_at(x0);
-  int64_t px = x0;       // tile index of the piece's end so far: px + (pp.t1 - pp.t0) is the next piece's start
   int pt = pp.t0;        // next tile of the piece
   int page_base = -32;   // tile of lane 0's page id
   int page_id = 0;
@@ -242,9 +258,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   auto request = [&]() {  // requests this warp's next unit, if the run has one; warp-uniform
     for (;;) {
       if (pt >= pp.t1) {
-        px += pp.t1 - pp.t0;
-        if (px >= x1) return;
-        pp = piece_at(px);
+        if (pp.next >= x1) return;
+        pp = piece_at(pp.next);
         pt = pp.t0;
         page_base = -32;
       }
@@ -282,7 +297,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   unsigned taken = 0;
   for (int64_t x = x0; x < x1;) {
     const Piece p = piece_at(x);
-    x += p.t1 - p.t0;
+    x = p.next;
+    if (p.t1 <= p.t0) continue;  // the cost of a pair whose tiles are the next run's
     const int64_t qb = (int64_t)p.b * a.q_sb + (int64_t)p.g * G * a.q_sh;
     uint32_t qa[kKS][2], qc[G16 ? kKS : 1][2];  // Q rows row (and row + 8) as MMA A operand
 #pragma unroll
@@ -397,12 +413,22 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         ldsm4_t(b, vt + (uint32_t)((pc >> 3) * L::kBox + v_row * 128 + (((pc & 7) ^ (v_row & 7)) << 4)));
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+          // a product of its own, added with rounding: the tensor core's
+          // accumulation truncates, which over thousands of units would show
+          float y[4] = {0.f, 0.f, 0.f, 0.f};
           if constexpr (G16) {
-            mma_16816(o[2 * d16 + u], hi[0][0], hi[0][1], hi[1][0], hi[1][1], b[2 * u], b[2 * u + 1]);
-            mma_16816(o[2 * d16 + u], lo[0][0], lo[0][1], lo[1][0], lo[1][1], b[2 * u], b[2 * u + 1]);
+            mma_16816(y, hi[0][0], hi[0][1], hi[1][0], hi[1][1], b[2 * u], b[2 * u + 1]);
+            mma_16816(y, lo[0][0], lo[0][1], lo[1][0], lo[1][1], b[2 * u], b[2 * u + 1]);
           } else {
-            mma_16816(o[2 * d16 + u], hi[0][0], lo[0][0], hi[1][0], lo[1][0], b[2 * u], b[2 * u + 1]);
+            mma_16816(y, hi[0][0], lo[0][0], hi[1][0], lo[1][0], b[2 * u], b[2 * u + 1]);
           }
+          float(&on)[4] = o[2 * d16 + u];
+          const float2 s01 = tc::add2(make_float2(on[0], on[1]), make_float2(y[0], y[1]));
+          const float2 s23 = tc::add2(make_float2(on[2], on[3]), make_float2(y[2], y[3]));
+          on[0] = s01.x;
+          on[1] = s01.y;
+          on[2] = s23.x;
+          on[3] = s23.y;
         }
       }
       __syncwarp();  // every lane has read the stage
@@ -494,8 +520,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       continue;
     }
     // ---- the last run of the pair joins the pieces
-    const int64_t pair0 = x - (p.t1 - p.t0) - p.t0;  // the pair's first tile
-    const int c0 = rs.of(pair0), c1 = rs.of(pair0 + p.nu - 1);
+    const int c0 = rs.of(p.pair), c1 = rs.of(p.pair + p.nu - 1);
     __threadfence();
     __syncthreads();
     uint32_t* ticket = a.tickets + (int64_t)p.b * Hkv + p.g;
