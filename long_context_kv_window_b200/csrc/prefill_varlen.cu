@@ -20,9 +20,12 @@
 // all that an SM's shared memory delivers, so P in shared memory (written,
 // then read back) would bound the kernel at two thirds of the MMA rate.
 //
-// The reference m moves only when a row's max passes it by more than 8 log2
-// units (p <= 2^8 otherwise); then the warp rescales its rows of O_i in TMEM:
-// S_i(t) was issued after O_i(t-1), so its completion means O_i is at rest.
+// The reference m is the row's max over its first key tile.  bf16 has the range
+// of fp32 and its precision does not depend on the size of p, so m need not
+// follow the max: later tiles take no max, and only when the sum of a tile
+// passes 2^40 does the reference move to the row's max and the warps rescale
+// their rows of O_i in TMEM (S_i(t) was issued after O_i(t-1), so its
+// completion means O_i is at rest).
 //
 // Keys a row does not see are masked before the max.  A masked value row still
 // meets p = 0 in the MMA, and 0 * inf = NaN; so the value tiles in which some
@@ -48,9 +51,9 @@ namespace kvc {
 namespace {
 
 constexpr int kVT = 128;          // rows per MMA tile, keys per key tile
-constexpr int kVBlock = 384;      // 12 warps
+constexpr int kVBlock = 640;      // 20 warps
 constexpr int kVMaxClean = 4;     // key tiles of a block in which some row masks a key: at most 3
-constexpr float kVSlack = 8.f;    // log2 units a row max may pass its reference by
+constexpr float kVMost = 0x1p40f;  // a tile's sum of a row (64 keys) past which its reference moves
 constexpr double kLn2 = 0.6931471805599453;
 constexpr double kLog2e = 1.4426950408889634;
 
@@ -68,6 +71,8 @@ struct VarArgs {
   int32_t* err;
 };
 
+constexpr int kVBarBytes = 2048;
+
 template <int D>
 struct VarSmem {
   static constexpr int kBlk = kVT * 128;         // 128 rows x 128 B: one 64-column block (16 KB)
@@ -75,7 +80,7 @@ struct VarSmem {
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kRing = 2 * kTile;        // Q: two tiles, then the K/V ring
   static constexpr int kBarOff = kRing + kStages * kTile;
-  static constexpr size_t kBytes = 1024 + (size_t)kBarOff + 1024;
+  static constexpr size_t kBytes = 1024 + (size_t)kBarOff + kVBarBytes;
   static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
 
@@ -87,6 +92,7 @@ struct VarBars {
   uint32_t tmem_base;
   int abort, dirty;
   int seq, blk;  // this CTA's sequence (-1: none) and block of it
+  float swap[2][kVT];  // [tile][row]: what the two threads of a row tell each other
 };
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -111,6 +117,31 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Barrier of `n` threads that also tells whether any of them said so.
+__device__ __forceinline__ bool named_bar_or(int id, int n, bool said) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(n), "r"((uint32_t)said)
+      : "memory");
+  return any != 0;
 }
 
 // MN-major operand descriptor, 128-byte swizzle: 64 MN-consecutive elements
@@ -144,7 +175,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   VarBars* bars = reinterpret_cast<VarBars*>(sm + L::kBarOff);
-  static_assert(sizeof(VarBars) <= 1024, "barrier block");
+  static_assert(sizeof(VarBars) <= kVBarBytes, "barrier block");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = (int)(blockIdx.x % (unsigned)a.Hkv);  // the heads of a block side by side
 
@@ -156,7 +187,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars->s_full[i], 1);
-      tc::mbar_init(&bars->p_full[i], 4);
+      tc::mbar_init(&bars->p_full[i], 8);
       tc::mbar_init(&bars->o_done[i], 1);
     }
     for (int i = 0; i < kVMaxClean; ++i) {
@@ -235,6 +266,9 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   const int nt = std::max(n_tiles[0], n_tiles[1]);
   int issued = 0;  // producer: K and V tiles requested
 
+  // registers: 384 x 168 at launch; the softmax warps take over what the others do not need
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == 0) {
     // ---- producer: Q, then K(0), V(0), K(1), V(1), ...
     if (lane == 0 && nt > 0) {
@@ -263,21 +297,24 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     // ---- MMA issuer: S of key tile 0, then for every key tile and MMA tile
     // the output and the next logits (which overwrite the P just used: the
     // tensor core runs them in the order they are issued)
-    if (lane == 0 && nt > 0) {
+    if (nt > 0) {
       const uint32_t id_s = tc::idesc_bf16_f32(128, 128);
       const uint32_t id_o = tc::idesc_bf16_f32(128, D) | (1u << 16);  // B (V) MN-major
       const uint64_t q_desc = tc::desc_k_sw128(tc::smem_u32(sm));
       const uint64_t k_desc = tc::desc_k_sw128(tc::smem_u32(sm + L::kRing));
       const uint64_t v_desc = desc_mn(tc::smem_u32(sm + L::kRing), (uint32_t)L::kBlk);
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) tc::mma_commit(bar);
+      };
       auto logits = [&](int i, int t) {
         const uint64_t qd = q_desc + (uint64_t)((uint32_t)(i * L::kTile) >> 4);
         const uint64_t kd = k_desc + (uint64_t)((uint32_t)(((2 * t) % L::kStages) * L::kTile) >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = (uint32_t)((ks >> 2) * L::kBlk + (ks & 3) * 32) >> 4;
-          tc::mma_bf16(tmem + (uint32_t)(128 * i), qd + off, kd + off, id_s, ks != 0);
+          if (elect_one()) tc::mma_bf16(tmem + (uint32_t)(128 * i), qd + off, kd + off, id_s, ks != 0);
         }
-        tc::mma_commit(&bars->s_full[i]);
+        commit(&bars->s_full[i]);
       };
       auto wait_full = [&](int j) { return tc::mbar_wait(&bars->full[j % L::kStages], (j / L::kStages) & 1, abort_flag); };
       bool ok = tc::mbar_wait(&bars->qfull, 0, abort_flag) && wait_full(0);
@@ -285,7 +322,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         tc::tc_fence_after();
         for (int i = 0; i < 2; ++i)
           if (n_tiles[i] > 0) logits(i, 0);
-        tc::mma_commit(&bars->empty[0]);  // K(0) is read
+        commit(&bars->empty[0]);  // K(0) is read
       }
       for (int t = 0; ok && t < nt; ++t) {
         const int vj = 2 * t + 1, vs = vj % L::kStages;
@@ -300,21 +337,22 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           const uint64_t vd = v_desc + (uint64_t)((uint32_t)(vs * L::kTile) >> 4);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)  // 16 keys: 8 columns of P, 16 value rows of 128 B
-            mma_bf16_ts(tmem + kO + (uint32_t)(D * i), tmem + (uint32_t)(128 * i + 8 * ks),
-                        vd + (uint64_t)((uint32_t)(ks * 16 * 128) >> 4), id_o, (t > 0 || ks > 0) ? 1u : 0u);
+            if (elect_one())
+              mma_bf16_ts(tmem + kO + (uint32_t)(D * i), tmem + (uint32_t)(128 * i + 8 * ks),
+                          vd + (uint64_t)((uint32_t)(ks * 16 * 128) >> 4), id_o, (t > 0 || ks > 0) ? 1u : 0u);
           if (t + 1 < n_tiles[i])
             logits(i, t + 1);
           else
-            tc::mma_commit(&bars->o_done[i]);
+            commit(&bars->o_done[i]);
         }
         if (!ok) break;
-        tc::mma_commit(&bars->empty[vs]);  // V(t) is read
-        if (t + 1 < nt) tc::mma_commit(&bars->empty[(vj + 1) % L::kStages]);  // and K(t + 1)
+        commit(&bars->empty[vs]);  // V(t) is read
+        if (t + 1 < nt) commit(&bars->empty[(vj + 1) % L::kStages]);  // and K(t + 1)
       }
-      tc::mma_commit(&bars->mma_done);  // every MMA issued above has completed before TMEM is freed
+      commit(&bars->mma_done);  // every MMA issued above has completed before TMEM is freed
       tc::mbar_drain(&bars->mma_done, 0);
     }
-  } else if (warp < 4) {
+  } else {
     // ---- value check: the tiles in which some row masks a key
     constexpr int kVec = L::kTile / 16;
     for (int t = t_mask; t < nt; ++t) {
@@ -344,9 +382,11 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars->clean[t - t_mask]);
     }
+  }
   } else {
-    // ---- softmax of one MMA tile, one row per thread
-    const int i = (warp - 4) >> 2, wq = warp & 3;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ---- softmax of one MMA tile, two threads per row: 64 keys of a tile each
+    const int i = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, wq = warp & 3;
     const int r = 32 * wq + lane;
     const int ti = i * a.nt + r / a.G;  // token of this row in the block
     const int h = g * a.G + r % a.G;
@@ -354,87 +394,104 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     const int limit = std::min(ti, lq - i0 - 1) + i0 + lk - lq;  // last key the row sees
     const int64_t row = (int64_t)(q0 + i0) + ti;                 // its row of out and lse
     const uint32_t lane_base = tmem + ((uint32_t)(32 * wq) << 16);
-    const uint32_t s_col = lane_base + (uint32_t)(128 * i), o_col = lane_base + kO + (uint32_t)(D * i);
+    const uint32_t s_col = lane_base + (uint32_t)(128 * i), o_col = lane_base + kO + (uint32_t)(D * i + (D / 2) * hf);
+    const int pair_bar = 1 + 4 * i + wq;  // named barrier of the two warps that share these rows
+    // f(x of half 0, x of half 1) for both threads of the row
+    volatile float* swap = &bars->swap[i][r];
+    auto both = [&](float mine_x, auto f) {
+      if (hf) *swap = mine_x;
+      tc::named_bar_sync(pair_bar, 64);
+      if (!hf) *swap = mine_x = f(mine_x, *swap);
+      tc::named_bar_sync(pair_bar, 64);
+      return hf ? *swap : mine_x;
+    };
     float m_ref = -INFINITY;
-    double l = 0.0;
+    double l = 0.0;  // this thread's half of the row sum
     bool ok = true;
-    for (int t = 0; t < n_tiles[i]; ++t) {
-      if (!tc::mbar_wait(&bars->s_full[i], t & 1, abort_flag)) { ok = false; break; }
-      __syncwarp();
-      tc::tc_fence_after();
-      uint32_t x[128];
-      {
-        uint32_t* x1 = x + 64;
-        KVC_TMEM_LD64(s_col, x);
-        KVC_TMEM_LD64(s_col + 64u, x1);
-        KVC_TMEM_WAIT_LD64(x);
-        KVC_TMEM_TIE32(x1);
-        uint32_t* x2 = x + 96;
-        KVC_TMEM_TIE32(x2);
-      }
+    uint32_t x[64];
+    auto load = [&](int t) {  // this thread's logits of key tile t, masked
+      KVC_TMEM_LD64(s_col + (uint32_t)(64 * hf), x);
+      KVC_TMEM_WAIT_LD64(x);
       if (t >= t_mask) {
-        const int lim = limit - t * kVT;  // the last visible column
+        const int lim = limit - t * kVT - 64 * hf;  // the last visible column
 #pragma unroll
-        for (int e = 0; e < kVT; ++e)
+        for (int e = 0; e < 64; ++e)
           if (e > lim) x[e] = __float_as_uint(-INFINITY);
       }
-      float mx = -INFINITY;
-#pragma unroll
-      for (int e = 0; e < kVT; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
-      const float mc = mx * a.c;
-      const bool move = mc > m_ref + kVSlack || (m_ref == -INFINITY && mc > -INFINITY);
-      float alpha = 1.f;
-      if (move) {
-        alpha = m_ref == -INFINITY ? 0.f : tc::ex2_approx(m_ref - mc);
-        l *= (double)alpha;
-        m_ref = mc;
-      }
-      if (t > 0 && __any_sync(0xffffffffu, move)) {
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t o[32];
-          KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
-          KVC_TMEM_WAIT_LD32(o);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(o_col + (uint32_t)c0, o);
-        }
-      }
+    };
+    auto probs = [&]() {  // p as bf16 pairs into x[0..32); returns their fp32 sum
       // a row that has seen no key yet has only x = -inf: p = 2^-inf = 0
       const float ref = m_ref == -INFINITY ? 0.f : m_ref;
       const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t w[32];
-#pragma unroll
-        for (int u = 0; u < 32; ++u) {
-          const int e = 64 * half + 2 * u;
-          const float2 y = tc::fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, nm2);
-          const float2 p = make_float2(tc::ex2_approx(y.x), tc::ex2_approx(y.y));
-          sum[u & 1] = tc::add2(sum[u & 1], p);
-          const __nv_bfloat162 hp = __floats2bfloat162_rn(p.x, p.y);
-          w[u] = *reinterpret_cast<const uint32_t*>(&hp);
-        }
-        tmem_st32(s_col + (uint32_t)(32 * half), w);
+      for (int u = 0; u < 32; ++u) {
+        const float2 y = tc::fma2(make_float2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), c2, nm2);
+        const float2 p = make_float2(tc::ex2_approx(y.x), tc::ex2_approx(y.y));
+        sum[u & 1] = tc::add2(sum[u & 1], p);
+        const __nv_bfloat162 hp = __floats2bfloat162_rn(p.x, p.y);
+        x[u] = *reinterpret_cast<const uint32_t*>(&hp);
       }
       const float2 s2 = tc::add2(sum[0], sum[1]);
-      l += (double)(s2.x + s2.y);
+      return s2.x + s2.y;
+    };
+    for (int t = 0; t < n_tiles[i]; ++t) {
+      if (!tc::mbar_wait(&bars->s_full[i], t & 1, abort_flag)) ok = false;
+      __syncwarp();
+      tc::tc_fence_after();
+      load(t);
+      float sum = 0.f;
+      bool fix = t == 0;  // the first tile sets the references
+      if (t > 0) {
+        sum = probs();
+        fix = named_bar_or(pair_bar, 64, sum > kVMost);  // also: both threads of a row hold their logits
+        if (fix) load(t);
+      }
+      if (fix) {
+        float mx[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(x[e]);
+#pragma unroll
+        for (int e = 4; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[e]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float mb = both(top * a.c, [](float x0, float x1) { return fmaxf(x0, x1); });
+        float alpha = 1.f;
+        if (mb > m_ref) {
+          alpha = m_ref == -INFINITY ? 0.f : tc::ex2_approx(m_ref - mb);
+          l *= (double)alpha;
+          m_ref = mb;
+        }
+        if (t > 0) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D / 2; c0 += 32) {
+            uint32_t o[32];
+            KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
+            KVC_TMEM_WAIT_LD32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(o_col + (uint32_t)c0, o);
+          }
+        }
+        sum = probs();
+      }
+      tmem_st32(s_col + (uint32_t)(32 * hf), *reinterpret_cast<const uint32_t(*)[32]>(x));
+      l += (double)sum;
       tmem_wait_st();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars->p_full[i]);
     }
-    // ---- the output rows and log-sum-exp
-    if (ok && n_tiles[i] > 0) ok = tc::mbar_wait(&bars->o_done[i], 0, abort_flag);
+    // ---- the output rows and log-sum-exp; the halves store a half of the columns each
+    if (n_tiles[i] > 0 && !tc::mbar_wait(&bars->o_done[i], 0, abort_flag)) ok = false;
     __syncwarp();
+    const float sum_row = both((float)l, [](float x0, float x1) { return x0 + x1; });
     if (ok && seq >= 0) {
       tc::tc_fence_after();
       const bool seen = limit >= 0;  // no key otherwise
-      const float inv = seen ? (float)(1.0 / l) : 0.f;
+      const float inv = seen ? 1.f / sum_row : 0.f;
       const bool dirty = *(volatile int*)&bars->dirty != 0;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
+      for (int c0 = 0; c0 < D / 2; c0 += 32) {
         uint32_t o[32];
         if (n_tiles[i] > 0) {
           KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
@@ -444,16 +501,17 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         float f[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) f[e] = seen ? __uint_as_float(o[e]) * inv : 0.f;
+        const int col = (D / 2) * hf + c0;
         if (dirty)  // non-finite values of the checked tiles, where this row sees them
           for (int j = t_mask * kVT; j <= limit; ++j) {
-            const uint16_t* vr = a.v + (int64_t)(k0 + j) * a.v_sn + (int64_t)g * a.v_sh + c0;
+            const uint16_t* vr = a.v + (int64_t)(k0 + j) * a.v_sn + (int64_t)g * a.v_sh + col;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const uint32_t bits = vr[e];
               if ((bits & 0x7F80u) == 0x7F80u) f[e] += __uint_as_float(bits << 16);
             }
           }
-        uint4* dst = reinterpret_cast<uint4*>(a.out + (row * a.H + h) * D + c0);
+        uint4* dst = reinterpret_cast<uint4*>(a.out + (row * a.H + h) * D + col);
 #pragma unroll
         for (int v8 = 0; v8 < 4; ++v8) {
           uint32_t w[4];
@@ -465,8 +523,8 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           dst[v8] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      if (mine && a.lse)
-        a.lse[row * a.H + h] = seen ? (float)(((double)m_ref + log2(l)) * kLn2) : -INFINITY;
+      if (mine && a.lse && hf == 0)
+        a.lse[row * a.H + h] = seen ? (float)(((double)m_ref + log2((double)sum_row)) * kLn2) : -INFINITY;
     }
   }
   tc::tc_fence_before();
