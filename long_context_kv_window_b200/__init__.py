@@ -12,6 +12,7 @@ inputs may be ``torch.bfloat16`` or raw ``int16``/``uint16`` bit patterns.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -585,6 +586,7 @@ def kvc_prefill_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, sca
     return out, lse
 
 
+@functools.lru_cache(maxsize=256)
 def prefill_varlen_workspace_size(H: int, Hkv: int, d: int, batch: int, total_q: int, max_q: int, max_k: int) -> int:
     out = ctypes.c_size_t(0)
     _check(lib().kvc_prefill_varlen_workspace_size(H, Hkv, d, batch, total_q, max_q, max_k, ctypes.byref(out)),
@@ -657,12 +659,14 @@ def kvc_prefill_attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     _dense(lse, "lse", (total_q, H), torch.float32, dev)
     _err_word(dev_err, dev)
     if ws is None:
-        ws = _scratch(prefill_varlen_workspace_size(H, Hkv, d, B, total_q, max_seqlen_q, max_seqlen_k), dev, stream)
+        need = prefill_varlen_workspace_size(H, Hkv, d, B, total_q, max_seqlen_q, max_seqlen_k)
+        ws = _scratch(need, dev, stream) if need else None
     sc = float(1.0 / math.sqrt(d) if scale is None else scale)
     _check(_call(dev, lib().kvc_prefill_attention_varlen, _adr(q), q.stride(0), q.stride(1), _adr(k), k.stride(0),
                  k.stride(1), _adr(v), v.stride(0), v.stride(1), _adr(cu_seqlens_q), _adr(cu_seqlens_k), B, total_q,
                  total_k, int(max_seqlen_q), int(max_seqlen_k), H, Hkv, d, sc, _adr(out), _adr(lse), _adr(ws),
-                 _ws_bytes(ws, dev), _adr(dev_err), _raw_stream(stream, dev)), "kvc_prefill_attention_varlen")
+                 0 if ws is None else _ws_bytes(ws, dev), _adr(dev_err), _raw_stream(stream, dev)),
+           "kvc_prefill_attention_varlen")
     _used_on(stream, made_out, made_lse)
     return out, lse
 

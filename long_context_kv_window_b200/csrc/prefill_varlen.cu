@@ -22,18 +22,24 @@
 //
 // The reference m is the row's max over its first key tile.  bf16 has the range
 // of fp32 and its precision does not depend on the size of p, so m need not
-// follow the max: later tiles take no max, and only when the sum of a tile
-// passes 2^40 does the reference move to the row's max and the warps rescale
-// their rows of O_i in TMEM (S_i(t) was issued after O_i(t-1), so its
-// completion means O_i is at rest).
+// follow the max: later tiles take no max.  Where a row's sum over 64 keys
+// passes 2^60 -- logits 41 above all of the first 128 keys -- the block is
+// computed again: a pass over the logits finds the rows' maxima, and the pass
+// after it uses those.
+//
+// P overwrites the logits it came from (the TMEM has no room for a second
+// buffer), so logits, softmax and output of an MMA tile follow one another, and
+// while one tile is at the tensor core the other is at its softmax.  Two
+// threads per row halve the time the softmax takes, and the output MMA of a
+// half starts when that half's P is there.
 //
 // Keys a row does not see are masked before the max.  A masked value row still
 // meets p = 0 in the MMA, and 0 * inf = NaN; so the value tiles in which some
 // row of the block masks a key are looked over first, infinities and NaN in
 // them are set to 0, and the rows that do see such a value add it at the end.
 //
-// Warps: 0 TMA producer, 1 MMA issuer (and TMEM), 2..3 value check, 4..7 and
-// 8..11 the softmax of tiles 0 and 1 (one row per thread).  Every wait is
+// Warps: 0 TMA producer, 1 and 2 MMA issuers of tiles 0 and 1 (1: TMEM), 3 value
+// check, 4..11 and 12..19 the softmax of tiles 0 and 1.  Every wait is
 // bounded; on a timeout the CTA records KVC_DEV_ERR_TIMEOUT, lets its copies
 // and MMAs land, frees TMEM and exits.
 #include <cuda.h>
@@ -53,7 +59,7 @@ namespace {
 constexpr int kVT = 128;          // rows per MMA tile, keys per key tile
 constexpr int kVBlock = 640;      // 20 warps
 constexpr int kVMaxClean = 4;     // key tiles of a block in which some row masks a key: at most 3
-constexpr float kVMost = 0x1p40f;  // a tile's sum of a row (64 keys) past which its reference moves
+constexpr float kVMost = 0x1p60f;  // a row's sum over 64 keys past which its reference is too far below its max
 constexpr double kLn2 = 0.6931471805599453;
 constexpr double kLog2e = 1.4426950408889634;
 
@@ -86,11 +92,11 @@ struct VarSmem {
 
 struct VarBars {
   uint64_t qfull, full[8], empty[8];
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t s_full[2], p_full[2], o_done[2], turn[2];
   uint64_t vland[kVMaxClean], clean[kVMaxClean];  // value tiles to be checked: landed, checked (used once each)
   uint64_t mma_done;
   uint32_t tmem_base;
-  int abort, dirty;
+  int abort, dirty, redo;
   int seq, blk;  // this CTA's sequence (-1: none) and block of it
   float swap[2][kVT];  // [tile][row]: what the two threads of a row tell each other
 };
@@ -128,20 +134,6 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
-}
-
-// Barrier of `n` threads that also tells whether any of them said so.
-__device__ __forceinline__ bool named_bar_or(int id, int n, bool said) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(any)
-      : "r"(id), "r"(n), "r"((uint32_t)said)
-      : "memory");
-  return any != 0;
 }
 
 // MN-major operand descriptor, 128-byte swizzle: 64 MN-consecutive elements
@@ -183,20 +175,22 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     tc::mbar_init(&bars->qfull, 1);
     for (int s = 0; s < L::kStages; ++s) {
       tc::mbar_init(&bars->full[s], 1);
-      tc::mbar_init(&bars->empty[s], 1);
+      tc::mbar_init(&bars->empty[s], 2);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars->s_full[i], 1);
       tc::mbar_init(&bars->p_full[i], 8);
       tc::mbar_init(&bars->o_done[i], 1);
+      tc::mbar_init(&bars->turn[i], 1);
     }
     for (int i = 0; i < kVMaxClean; ++i) {
       tc::mbar_init(&bars->vland[i], 1);
-      tc::mbar_init(&bars->clean[i], 2);
+      tc::mbar_init(&bars->clean[i], 1);
     }
-    tc::mbar_init(&bars->mma_done, 1);
+    tc::mbar_init(&bars->mma_done, 2);
     bars->abort = 0;
     bars->dirty = 0;
+    bars->redo = 0;
     tc::fence_mbar_init();
     tc::prefetch_tmap(&qmap);
     tc::prefetch_tmap(&kmap);
@@ -214,28 +208,39 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   tc::fence_proxy_async_smem();
   pdl_wait();  // the inputs may come from the previous kernel of the stream
   if (warp == 2) {
-    // the block of this CTA: sequences in order, the last (longest) block of
-    // each first; the first CTA looks at every sequence, for the error word
+    // the block of this CTA: up to 32 sequences the longest first, more in
+    // order; the last (longest) block of each first.  Four chunks of 512
+    // queries over 8K to 32K keys: 1000 us in order, SORTED us sorted.  The
+    // first CTA looks at every sequence, for the error word.
     const bool first = blockIdx.x == 0;
     int left = (int)(blockIdx.x / (unsigned)a.Hkv), found = -1, blk = 0;
     for (int b0 = 0; b0 < a.batch && (found < 0 || first); b0 += 32) {
       bool bad = false;
       const int nb = b0 + lane < a.batch ? seq_blocks(a, b0 + lane, &bad) : 0;
       if (bad && first) set_dev_err(a.err, KVC_DEV_ERR_SEQLENS);
-      int inc = nb;
+      int before = 0;  // blocks of the sequences that come before this lane's
+      if (a.batch <= 32) {
+        const int keys = nb > 0 ? a.cu_k[lane + 1] - a.cu_k[lane] : -1;
+        for (int j = 0; j < a.batch; ++j) {
+          const int kj = __shfl_sync(0xffffffffu, keys, j), nj = __shfl_sync(0xffffffffu, nb, j);
+          if (kj > keys || (kj == keys && j < lane)) before += nj;
+        }
+      } else {
+        int inc = nb;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        before = inc - nb;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, inc > left);
+      const unsigned hit = __ballot_sync(0xffffffffu, left >= before && left < before + nb);
       if (hit && found < 0) {
         const int src = __ffs(hit) - 1;
-        const int nbs = __shfl_sync(0xffffffffu, nb, src), before = __shfl_sync(0xffffffffu, inc - nb, src);
         found = b0 + src;
-        blk = nbs - 1 - (left - before);
+        blk = __shfl_sync(0xffffffffu, nb, src) - 1 - (left - __shfl_sync(0xffffffffu, before, src));
       }
-      left -= __shfl_sync(0xffffffffu, inc, 31);
+      left -= __reduce_add_sync(0xffffffffu, nb);
     }
     if (lane == 0) {
       bars->seq = found;
@@ -248,8 +253,8 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort;
   const int seq = bars->seq;
-  int n_tiles[2] = {0, 0};  // key tiles up to the last row of each MMA tile
-  int t_mask = 0;           // first key tile in which some row of the block masks a key
+  int nt = 0;      // key tiles up to the block's last row
+  int t_mask = 0;  // first key tile in which some row of the block masks a key
   int q0 = 0, k0 = 0, lq = 0, lk = 0, i0 = 0;
   if (seq >= 0) {
     q0 = a.cu_q[seq];
@@ -257,135 +262,166 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     lq = a.cu_q[seq + 1] - q0;
     lk = a.cu_k[seq + 1] - k0;
     i0 = bars->blk * 2 * a.nt;
-    for (int i = 0; i < 2; ++i) {
-      const int lim = std::min(lq - i0, (i + 1) * a.nt) - 1 + i0 + lk - lq;  // the tile's last row sees keys up to here
-      n_tiles[i] = i * a.nt < lq - i0 && lim >= 0 ? lim / kVT + 1 : 0;
-    }
+    const int lim = std::min(lq - i0, 2 * a.nt) - 1 + i0 + lk - lq;  // the last row sees keys up to here
+    nt = lim >= 0 ? lim / kVT + 1 : 0;
     t_mask = std::max(0, i0 + lk - lq + 1) / kVT;
   }
-  const int nt = std::max(n_tiles[0], n_tiles[1]);
-  int issued = 0;  // producer: K and V tiles requested
+  int issued = 0, last_pass = 0;  // producer: K and V tiles requested
+  // Pass 0 computes; if a row passed its reference by too much, pass 1 finds
+  // every row's max and pass 2 computes with that.  The ring and the barriers
+  // go on counting from pass to pass.
+  auto again = [&](int pass) {
+    tc::named_bar_sync(15, kVBlock);
+    if (*abort_flag) return false;
+    return pass == 0 ? *(volatile int*)&bars->redo != 0 : pass == 1;
+  };
+  auto ring_base = [&](int pass) { return pass == 0 ? 0 : pass == 1 ? 2 * nt : 3 * nt; };
 
-  // registers: 384 x 168 at launch; the softmax warps take over what the others do not need
+  // registers: 640 x 96 at launch; the softmax warps take over what the others do not need
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-  if (warp == 0) {
-    // ---- producer: Q, then K(0), V(0), K(1), V(1), ...
-    if (lane == 0 && nt > 0) {
-      tc::mbar_arrive_expect_tx(&bars->qfull, (uint32_t)(2 * kCB * a.nt * a.G * 128));
-      for (int i = 0; i < 2; ++i)
-        for (int cb = 0; cb < kCB; ++cb)
-          tc::tma_load_3d(sm + i * L::kTile + cb * L::kBlk, &qmap, &bars->qfull, cb * 64, g * a.G,
-                          q0 + i0 + i * a.nt);
-      for (int j = 0; j < 2 * nt; ++j) {
-        const int s = j % L::kStages;
-        if (j >= L::kStages && !tc::mbar_wait(&bars->empty[s], ((j / L::kStages) - 1) & 1, abort_flag)) break;
-        // a value tile to be checked lands on a barrier of its own, which its
-        // readers can wait for without following the ring's phases
-        const int t = j >> 1;
-        const bool checked = (j & 1) && t >= t_mask;
-        uint64_t* land = checked ? &bars->vland[t - t_mask] : &bars->full[s];
-        if (checked) tc::mbar_arrive(&bars->full[s]);
-        tc::mbar_arrive_expect_tx(land, (uint32_t)L::kTile);
-        for (int cb = 0; cb < kCB; ++cb)
-          tc::tma_load_3d(sm + L::kRing + s * L::kTile + cb * L::kBlk, (j & 1) ? &vmap : &kmap, land, cb * 64, g,
-                          k0 + t * kVT);
-        issued = j + 1;
+    if (warp == 0) {
+      // ---- producer: Q, then K(0), V(0), K(1), V(1), ... (pass 1: K alone)
+      if (lane == 0 && nt > 0) {
+        tc::mbar_arrive_expect_tx(&bars->qfull, (uint32_t)(2 * kCB * a.nt * a.G * 128));
+        for (int i = 0; i < 2; ++i)
+          for (int cb = 0; cb < kCB; ++cb)
+            tc::tma_load_3d(sm + i * L::kTile + cb * L::kBlk, &qmap, &bars->qfull, cb * 64, g * a.G,
+                            q0 + i0 + i * a.nt);
       }
-    }
-  } else if (warp == 1) {
-    // ---- MMA issuer: S of key tile 0, then for every key tile and MMA tile
-    // the output and the next logits (which overwrite the P just used: the
-    // tensor core runs them in the order they are issued)
-    if (nt > 0) {
+      for (int pass = 0; pass == 0 || again(pass - 1); ++pass) {
+        const int count = lane != 0 ? 0 : pass == 1 ? nt : 2 * nt;
+        last_pass = pass;
+        for (int j = 0; j < count; ++j, ++issued) {
+          const int s = issued % L::kStages;
+          if (issued >= L::kStages && !tc::mbar_wait(&bars->empty[s], ((issued / L::kStages) - 1) & 1, abort_flag)) break;
+          // a value tile to be checked lands on a barrier of its own, which its
+          // readers can wait for without following the ring's phases
+          const int t = pass == 1 ? j : j >> 1;
+          const bool value = pass != 1 && (j & 1), checked = value && t >= t_mask;
+          uint64_t* land = checked ? &bars->vland[t - t_mask] : &bars->full[s];
+          if (checked) tc::mbar_arrive(&bars->full[s]);
+          tc::mbar_arrive_expect_tx(land, (uint32_t)L::kTile);
+          for (int cb = 0; cb < kCB; ++cb)
+            tc::tma_load_3d(sm + L::kRing + s * L::kTile + cb * L::kBlk, value ? &vmap : &kmap, land, cb * 64, g,
+                            k0 + t * kVT);
+        }
+        __syncwarp();
+      }
+    } else if (warp < 3) {
+      // ---- MMA issuers, one per MMA tile: S of key tile 0, then for every key
+      // tile the output and the next logits (which overwrite the P just used:
+      // the tensor core runs a thread's MMAs in the order they are issued).
+      // The tensor core queues hardly ahead, so what a warp spends on waits and
+      // commits would leave it idle; the other tile's MMAs fill that.  They
+      // take turns, the next one invited two MMAs early: mixed, both tiles'
+      // MMAs would end late and both softmaxes run while the tensor core waits.
+      // Stages are released by the softmax warps, which learn from S(t) that
+      // everything before it is done: a commit costs the pipe about 100 cycles.
+      const int i = warp - 1;
       const uint32_t id_s = tc::idesc_bf16_f32(128, 128);
       const uint32_t id_o = tc::idesc_bf16_f32(128, D) | (1u << 16);  // B (V) MN-major
-      const uint64_t q_desc = tc::desc_k_sw128(tc::smem_u32(sm));
+      const uint64_t q_desc = tc::desc_k_sw128(tc::smem_u32(sm + i * L::kTile));
       const uint64_t k_desc = tc::desc_k_sw128(tc::smem_u32(sm + L::kRing));
       const uint64_t v_desc = desc_mn(tc::smem_u32(sm + L::kRing), (uint32_t)L::kBlk);
+      const uint32_t s_tmem = tmem + (uint32_t)(128 * i), o_tmem = tmem + kO + (uint32_t)(D * i);
       auto commit = [&](uint64_t* bar) {
         if (elect_one()) tc::mma_commit(bar);
       };
-      auto logits = [&](int i, int t) {
-        const uint64_t qd = q_desc + (uint64_t)((uint32_t)(i * L::kTile) >> 4);
-        const uint64_t kd = k_desc + (uint64_t)((uint32_t)(((2 * t) % L::kStages) * L::kTile) >> 4);
+      int turns = 0;  // groups issued
+      auto my_turn = [&]() { return (i == 0 && turns == 0) || tc::mbar_wait(&bars->turn[i], (turns - (i == 0)) & 1, abort_flag); };
+      auto your_turn = [&]() {
+        ++turns;
+        if (elect_one()) tc::mbar_arrive(&bars->turn[i ^ 1]);
+      };
+      auto logits = [&](int s) {  // S from the K tile in stage s
+        const uint64_t kd = k_desc + (uint64_t)((uint32_t)(s * L::kTile) >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = (uint32_t)((ks >> 2) * L::kBlk + (ks & 3) * 32) >> 4;
-          if (elect_one()) tc::mma_bf16(tmem + (uint32_t)(128 * i), qd + off, kd + off, id_s, ks != 0);
+          if (ks == D / 16 - 2) your_turn();
+          if (elect_one()) tc::mma_bf16(s_tmem, q_desc + off, kd + off, id_s, ks != 0);
         }
         commit(&bars->s_full[i]);
       };
       auto wait_full = [&](int j) { return tc::mbar_wait(&bars->full[j % L::kStages], (j / L::kStages) & 1, abort_flag); };
-      bool ok = tc::mbar_wait(&bars->qfull, 0, abort_flag) && wait_full(0);
-      if (ok) {
-        tc::tc_fence_after();
-        for (int i = 0; i < 2; ++i)
-          if (n_tiles[i] > 0) logits(i, 0);
-        commit(&bars->empty[0]);  // K(0) is read
-      }
-      for (int t = 0; ok && t < nt; ++t) {
-        const int vj = 2 * t + 1, vs = vj % L::kStages;
-        ok = wait_full(vj);
-        if (ok && t >= t_mask) ok = tc::mbar_wait(&bars->clean[t - t_mask], 0, abort_flag);
-        if (ok && t + 1 < nt) ok = wait_full(vj + 1);
-        for (int i = 0; ok && i < 2; ++i) {
-          if (t >= n_tiles[i]) continue;
-          ok = tc::mbar_wait(&bars->p_full[i], t & 1, abort_flag);
+      for (int pass = 0; pass == 0 || again(pass - 1); ++pass) {
+        if (nt == 0) continue;
+        const int base = ring_base(pass);
+        const bool maxes = pass == 1;
+        bool ok = (pass > 0 || tc::mbar_wait(&bars->qfull, 0, abort_flag)) && wait_full(base) && my_turn();
+        if (ok) {
+          tc::tc_fence_after();
+          logits(base % L::kStages);
+        }
+        for (int t = 0; ok && t < nt; ++t) {
+          const int vj = base + 2 * t + 1, vs = vj % L::kStages;               // V(t)
+          const int kj = maxes ? base + t + 1 : vj + 1, ks_ = kj % L::kStages;  // K(t + 1)
+          if (!maxes) {
+            ok = wait_full(vj);
+            if (ok && t >= t_mask) ok = tc::mbar_wait(&bars->clean[t - t_mask], pass >> 1, abort_flag);
+          }
+          if (ok && t + 1 < nt) ok = wait_full(kj);
+          if (ok) ok = tc::mbar_wait(&bars->p_full[i], (pass * nt + t) & 1, abort_flag);
+          if (ok) ok = my_turn();
           if (!ok) break;
           tc::tc_fence_after();
-          const uint64_t vd = v_desc + (uint64_t)((uint32_t)(vs * L::kTile) >> 4);
+          if (!maxes) {
+            const uint64_t vd = v_desc + (uint64_t)((uint32_t)(vs * L::kTile) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)  // 16 keys: 8 columns of P, 16 value rows of 128 B
-            if (elect_one())
-              mma_bf16_ts(tmem + kO + (uint32_t)(D * i), tmem + (uint32_t)(128 * i + 8 * ks),
-                          vd + (uint64_t)((uint32_t)(ks * 16 * 128) >> 4), id_o, (t > 0 || ks > 0) ? 1u : 0u);
-          if (t + 1 < n_tiles[i])
-            logits(i, t + 1);
-          else
-            commit(&bars->o_done[i]);
+            for (int ks = 0; ks < 8; ++ks)  // 16 keys: 8 columns of P (64 keys over each half of S), 16 value rows of 128 B
+              if (elect_one())
+                mma_bf16_ts(o_tmem, s_tmem + (uint32_t)(64 * (ks >> 2) + 8 * (ks & 3)),
+                            vd + (uint64_t)((uint32_t)(ks * 16 * 128) >> 4), id_o, (t > 0 || ks > 0) ? 1u : 0u);
+          }
+          if (t + 1 < nt) {
+            logits(ks_);
+          } else {
+            your_turn();
+            if (!maxes) commit(&bars->o_done[i]);
+          }
         }
-        if (!ok) break;
-        commit(&bars->empty[vs]);  // V(t) is read
-        if (t + 1 < nt) commit(&bars->empty[(vj + 1) % L::kStages]);  // and K(t + 1)
       }
       commit(&bars->mma_done);  // every MMA issued above has completed before TMEM is freed
       tc::mbar_drain(&bars->mma_done, 0);
-    }
-  } else {
-    // ---- value check: the tiles in which some row masks a key
-    constexpr int kVec = L::kTile / 16;
-    for (int t = t_mask; t < nt; ++t) {
-      const int s = (2 * t + 1) % L::kStages;
-      if (!tc::mbar_wait(&bars->vland[t - t_mask], 0, abort_flag)) break;
-      uint4* tile = reinterpret_cast<uint4*>(sm + L::kRing + s * L::kTile);
-      uint32_t top = 0;  // the largest magnitude, per 16-bit half
+    } else {
+      // ---- value check: the tiles in which some row masks a key
+      constexpr int kVec = L::kTile / 16;
+      for (int pass = 0; pass == 0 || again(pass - 1); ++pass) {
+        if (pass == 1) continue;
+        for (int t = t_mask; t < nt; ++t) {
+          const int s = (ring_base(pass) + 2 * t + 1) % L::kStages;
+          if (!tc::mbar_wait(&bars->vland[t - t_mask], pass >> 1, abort_flag)) break;
+          uint4* tile = reinterpret_cast<uint4*>(sm + L::kRing + s * L::kTile);
+          uint32_t top = 0;  // the largest magnitude, per 16-bit half
 #pragma unroll 8
-      for (int i = tid - 64; i < kVec; i += 64) {
-        const uint4 w = tile[i];
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                     __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
-      }
-      if ((top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u) {
-        bars->dirty = 1;
-        for (int i = tid - 64; i < kVec; i += 64) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(tile + i);
-          for (int u = 0; u < 4; ++u) {
-            uint32_t x = w[u];
-            if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
-            if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
-            w[u] = x;
+          for (int i = lane; i < kVec; i += 32) {
+            const uint4 w = tile[i];
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                         __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
           }
+          if ((top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u) {
+            bars->dirty = 1;
+            for (int i = lane; i < kVec; i += 32) {
+              uint32_t* w = reinterpret_cast<uint32_t*>(tile + i);
+              for (int u = 0; u < 4; ++u) {
+                uint32_t x = w[u];
+                if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+                if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
+                w[u] = x;
+              }
+            }
+            tc::fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bars->clean[t - t_mask]);
         }
-        tc::fence_proxy_async_smem();
       }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars->clean[t - t_mask]);
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    // ---- softmax of one MMA tile, two threads per row: 64 keys of a tile each
+    // ---- softmax of one MMA tile, two threads per row: 64 keys of a key tile
+    // each, P over the first half of the logits they came from
     const int i = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, wq = warp & 3;
     const int r = 32 * wq + lane;
     const int ti = i * a.nt + r / a.G;  // token of this row in the block
@@ -394,7 +430,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     const int limit = std::min(ti, lq - i0 - 1) + i0 + lk - lq;  // last key the row sees
     const int64_t row = (int64_t)(q0 + i0) + ti;                 // its row of out and lse
     const uint32_t lane_base = tmem + ((uint32_t)(32 * wq) << 16);
-    const uint32_t s_col = lane_base + (uint32_t)(128 * i), o_col = lane_base + kO + (uint32_t)(D * i + (D / 2) * hf);
+    const uint32_t s_col = lane_base + (uint32_t)(128 * i + 64 * hf), o_col = lane_base + kO + (uint32_t)(D * i + (D / 2) * hf);
     const int pair_bar = 1 + 4 * i + wq;  // named barrier of the two warps that share these rows
     // f(x of half 0, x of half 1) for both threads of the row
     volatile float* swap = &bars->swap[i][r];
@@ -405,84 +441,81 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       tc::named_bar_sync(pair_bar, 64);
       return hf ? *swap : mine_x;
     };
+    auto larger = [](float x0, float x1) { return fmaxf(x0, x1); };
     float m_ref = -INFINITY;
     double l = 0.0;  // this thread's half of the row sum
     bool ok = true;
     uint32_t x[64];
-    auto load = [&](int t) {  // this thread's logits of key tile t, masked
-      KVC_TMEM_LD64(s_col + (uint32_t)(64 * hf), x);
-      KVC_TMEM_WAIT_LD64(x);
-      if (t >= t_mask) {
-        const int lim = limit - t * kVT - 64 * hf;  // the last visible column
+    auto row_max = [&]() {  // of this thread's logits, in log2 units
+      float mx[4];
 #pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (e > lim) x[e] = __float_as_uint(-INFINITY);
-      }
+      for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(x[e]);
+#pragma unroll
+      for (int e = 4; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[e]));
+      return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
     };
-    auto probs = [&]() {  // p as bf16 pairs into x[0..32); returns their fp32 sum
-      // a row that has seen no key yet has only x = -inf: p = 2^-inf = 0
-      const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-      const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int u = 0; u < 32; ++u) {
-        const float2 y = tc::fma2(make_float2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), c2, nm2);
-        const float2 p = make_float2(tc::ex2_approx(y.x), tc::ex2_approx(y.y));
-        sum[u & 1] = tc::add2(sum[u & 1], p);
-        const __nv_bfloat162 hp = __floats2bfloat162_rn(p.x, p.y);
-        x[u] = *reinterpret_cast<const uint32_t*>(&hp);
-      }
-      const float2 s2 = tc::add2(sum[0], sum[1]);
-      return s2.x + s2.y;
-    };
-    for (int t = 0; t < n_tiles[i]; ++t) {
-      if (!tc::mbar_wait(&bars->s_full[i], t & 1, abort_flag)) ok = false;
-      __syncwarp();
-      tc::tc_fence_after();
-      load(t);
-      float sum = 0.f;
-      bool fix = t == 0;  // the first tile sets the references
-      if (t > 0) {
-        sum = probs();
-        fix = named_bar_or(pair_bar, 64, sum > kVMost);  // also: both threads of a row hold their logits
-        if (fix) load(t);
-      }
-      if (fix) {
-        float mx[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(x[e]);
-#pragma unroll
-        for (int e = 4; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[e]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float mb = both(top * a.c, [](float x0, float x1) { return fmaxf(x0, x1); });
-        float alpha = 1.f;
-        if (mb > m_ref) {
-          alpha = m_ref == -INFINITY ? 0.f : tc::ex2_approx(m_ref - mb);
-          l *= (double)alpha;
-          m_ref = mb;
-        }
-        if (t > 0) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < D / 2; c0 += 32) {
-            uint32_t o[32];
-            KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
-            KVC_TMEM_WAIT_LD32(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(o_col + (uint32_t)c0, o);
+    const bool releases = wq == 0 && hf == 0 && lane == 0;  // tells the producer for this tile
+    for (int pass = 0; pass == 0 || again(pass - 1); ++pass) {
+      const int ub = pass * nt, base = ring_base(pass);
+      bool past = false;
+      l = 0.0;
+      if (pass == 1) m_ref = -INFINITY;
+      for (int t = 0; t < nt; ++t) {
+        if (!tc::mbar_wait(&bars->s_full[i], (ub + t) & 1, abort_flag)) ok = false;
+        if (releases) {  // S(t) is there: K(t) and, before it, V(t - 1) are read
+          if (pass == 1) {
+            tc::mbar_arrive(&bars->empty[(base + t) % L::kStages]);
+          } else {
+            tc::mbar_arrive(&bars->empty[(base + 2 * t) % L::kStages]);
+            if (t > 0) tc::mbar_arrive(&bars->empty[(base + 2 * t - 1) % L::kStages]);
           }
         }
-        sum = probs();
+        __syncwarp();
+        tc::tc_fence_after();
+        KVC_TMEM_LD64(s_col, x);
+        KVC_TMEM_WAIT_LD64(x);
+        if (t >= t_mask) {
+          const int lim = limit - t * kVT - 64 * hf;  // the last visible column
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e > lim) x[e] = __float_as_uint(-INFINITY);
+        }
+        if (pass == 1) {
+          m_ref = fmaxf(m_ref, row_max());
+        } else {
+          if (pass == 0 && t == 0) m_ref = both(row_max(), larger);  // the first tile sets the references
+          // a row that has seen no key yet has only x = -inf: p = 2^-inf = 0
+          const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+          const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            const float2 y = tc::fma2(make_float2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), c2, nm2);
+            const float2 p = make_float2(tc::ex2_approx(y.x), tc::ex2_approx(y.y));
+            sum[u & 1] = tc::add2(sum[u & 1], p);
+            const __nv_bfloat162 hp = __floats2bfloat162_rn(p.x, p.y);
+            x[u] = *reinterpret_cast<const uint32_t*>(&hp);
+          }
+          tmem_st32(s_col, *reinterpret_cast<const uint32_t(*)[32]>(x));
+          const float2 s2 = tc::add2(sum[0], sum[1]);
+          const float s = s2.x + s2.y;
+          past |= s > kVMost;
+          l += (double)s;
+          tmem_wait_st();
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->p_full[i]);
       }
-      tmem_st32(s_col + (uint32_t)(32 * hf), *reinterpret_cast<const uint32_t(*)[32]>(x));
-      l += (double)sum;
-      tmem_wait_st();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bars->p_full[i]);
+      if (pass == 1) {
+        m_ref = both(m_ref, larger);
+      } else {
+        if (nt > 0 && !tc::mbar_wait(&bars->o_done[i], pass >> 1, abort_flag)) ok = false;
+        if (nt > 0 && releases) tc::mbar_arrive(&bars->empty[(base + 2 * nt - 1) % L::kStages]);
+        if (pass == 0 && past && mine) bars->redo = 1;
+      }
     }
     // ---- the output rows and log-sum-exp; the halves store a half of the columns each
-    if (n_tiles[i] > 0 && !tc::mbar_wait(&bars->o_done[i], 0, abort_flag)) ok = false;
     __syncwarp();
     const float sum_row = both((float)l, [](float x0, float x1) { return x0 + x1; });
     if (ok && seq >= 0) {
@@ -493,7 +526,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 #pragma unroll 1
       for (int c0 = 0; c0 < D / 2; c0 += 32) {
         uint32_t o[32];
-        if (n_tiles[i] > 0) {
+        if (nt > 0) {
           KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
           KVC_TMEM_WAIT_LD32(o);
         }
@@ -533,10 +566,9 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     set_dev_err(a.err, KVC_DEV_ERR_TIMEOUT);
     if (issued > 0) tc::mbar_drain(&bars->qfull, 0);
     for (int j = std::max(0, issued - L::kStages); j < issued; ++j)
-      if ((j & 1) && (j >> 1) >= t_mask)
-        tc::mbar_drain(&bars->vland[(j >> 1) - t_mask], 0);
-      else
-        tc::mbar_drain(&bars->full[j % L::kStages], (j / L::kStages) & 1);
+      tc::mbar_drain(&bars->full[j % L::kStages], (j / L::kStages) & 1);
+    for (int t = t_mask; last_pass != 1 && t < nt; ++t)
+      if (issued > ring_base(last_pass) + 2 * t + 1) tc::mbar_drain(&bars->vland[t - t_mask], last_pass >> 1);
   }
   if (warp == 1) {
     tc::tc_fence_after();

@@ -112,6 +112,26 @@ def test_prefill_varlen_reference_moves(G, d):
     _close(_np(out), w_out, tol, "out")
 
 
+@pytest.mark.parametrize("n,at,G", [(700, 650, 4), (700, 130, 1), (1200, 1199, 2), (300, 299, 5)])
+def test_prefill_varlen_logits_far_above_the_first_tile(n, at, G):
+    """Logits hundreds above everything in the first 128 keys (the block is
+    computed again with the rows' maxima); later rows see them, earlier do not."""
+    rng = np.random.default_rng(n + at)
+    d = 128
+    q, _ = _bf16(rng, n, G, d)
+    q = np.abs(q)
+    k, _ = _bf16(rng, n, 1, d, scale=0.1)
+    k[at, 0] = 32.0  # scale * q . k of about 32 * 0.8 * sqrt(128) = 290
+    k[at // 2, 0] = -16.0
+    v, vd = _bf16(rng, n, 1, d)
+    qd, kd = (torch.from_numpy(x).to(torch.bfloat16).cuda() for x in (q, k))
+    out, lse = _run_prefill(qd, kd, vd, [n], [n])
+    w_out, w_lse, tol, tol_lse = ref.prefill_varlen(q, k, v, [0, n], [0, n], 1 / math.sqrt(d))
+    assert w_lse.max() > 200
+    _close(_np(lse), w_lse, tol_lse, "lse")
+    _close(_np(out), w_out, tol, "out")
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_prefill_varlen_fused_projection_views_and_rows_behind(d):
     """q, k, v as views of one [n][(H + 2 Hkv) d] projection; rows behind the
