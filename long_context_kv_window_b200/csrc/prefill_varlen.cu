@@ -72,6 +72,9 @@ struct VarArgs {
   int batch, H, Hkv, G;
   int nt;                // tokens per tile: 128 / G
   float c;               // scale * log2(e)
+  int splits;            // CTAs that share the keys of a block
+  float* part_z;         // splits > 1: [splits][total_q][H] log-sum-exp of the split, log2 units
+  float* part_o;         // splits > 1: [splits][total_q][H][D] its output
   uint16_t* out;         // [total_q][H][D] or nullptr
   float* lse;            // [total_q][H] or nullptr
   int32_t* err;
@@ -169,7 +172,8 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   VarBars* bars = reinterpret_cast<VarBars*>(sm + L::kBarOff);
   static_assert(sizeof(VarBars) <= kVBarBytes, "barrier block");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = (int)(blockIdx.x % (unsigned)a.Hkv);  // the heads of a block side by side
+  const int split = (int)(blockIdx.x % (unsigned)a.splits);  // the splits of a block side by side, then its heads
+  const int g = (int)(blockIdx.x / (unsigned)a.splits % (unsigned)a.Hkv);
 
   if (tid == 0) {
     tc::mbar_init(&bars->qfull, 1);
@@ -210,10 +214,10 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   if (warp == 2) {
     // the block of this CTA: up to 32 sequences the longest first, more in
     // order; the last (longest) block of each first.  Four chunks of 512
-    // queries over 8K to 32K keys: 1000 us in order, SORTED us sorted.  The
+    // queries over 8K to 32K keys: 1010 us in order, 836 us sorted.  The
     // first CTA looks at every sequence, for the error word.
     const bool first = blockIdx.x == 0;
-    int left = (int)(blockIdx.x / (unsigned)a.Hkv), found = -1, blk = 0;
+    int left = (int)(blockIdx.x / (unsigned)a.splits / (unsigned)a.Hkv), found = -1, blk = 0;
     for (int b0 = 0; b0 < a.batch && (found < 0 || first); b0 += 32) {
       bool bad = false;
       const int nb = b0 + lane < a.batch ? seq_blocks(a, b0 + lane, &bad) : 0;
@@ -253,8 +257,9 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort;
   const int seq = bars->seq;
-  int nt = 0;      // key tiles up to the block's last row
-  int t_mask = 0;  // first key tile in which some row of the block masks a key
+  int nt = 0;      // key tiles of this CTA: up to the block's last row, or its share of them
+  int t_mask = 0;  // first of them in which some row of the block masks a key
+  int kf = 0;      // first key of the first of them
   int q0 = 0, k0 = 0, lq = 0, lk = 0, i0 = 0;
   if (seq >= 0) {
     q0 = a.cu_q[seq];
@@ -264,7 +269,10 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     i0 = bars->blk * 2 * a.nt;
     const int lim = std::min(lq - i0, 2 * a.nt) - 1 + i0 + lk - lq;  // the last row sees keys up to here
     nt = lim >= 0 ? lim / kVT + 1 : 0;
-    t_mask = std::max(0, i0 + lk - lq + 1) / kVT;
+    const int t0 = (int)((int64_t)nt * split / a.splits);
+    nt = (int)((int64_t)nt * (split + 1) / a.splits) - t0;
+    t_mask = std::max(0, std::max(0, i0 + lk - lq + 1) / kVT - t0);
+    kf = t0 * kVT;
   }
   int issued = 0, last_pass = 0;  // producer: K and V tiles requested
   // Pass 0 computes; if a row passed its reference by too much, pass 1 finds
@@ -304,7 +312,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           tc::mbar_arrive_expect_tx(land, (uint32_t)L::kTile);
           for (int cb = 0; cb < kCB; ++cb)
             tc::tma_load_3d(sm + L::kRing + s * L::kTile + cb * L::kBlk, value ? &vmap : &kmap, land, cb * 64, g,
-                            k0 + t * kVT);
+                            k0 + kf + t * kVT);
         }
         __syncwarp();
       }
@@ -475,7 +483,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         KVC_TMEM_LD64(s_col, x);
         KVC_TMEM_WAIT_LD64(x);
         if (t >= t_mask) {
-          const int lim = limit - t * kVT - 64 * hf;  // the last visible column
+          const int lim = limit - kf - t * kVT - 64 * hf;  // the last visible column
 #pragma unroll
           for (int e = 0; e < 64; ++e)
             if (e > lim) x[e] = __float_as_uint(-INFINITY);
@@ -520,7 +528,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     const float sum_row = both((float)l, [](float x0, float x1) { return x0 + x1; });
     if (ok && seq >= 0) {
       tc::tc_fence_after();
-      const bool seen = limit >= 0;  // no key otherwise
+      const bool seen = limit >= kf && nt > 0;  // no key of this CTA otherwise
       const float inv = seen ? 1.f / sum_row : 0.f;
       const bool dirty = *(volatile int*)&bars->dirty != 0;
 #pragma unroll 1
@@ -530,13 +538,13 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
           KVC_TMEM_WAIT_LD32(o);
         }
-        if (!mine || !a.out) continue;
+        if (!mine || (!a.out && !a.part_o)) continue;
         float f[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) f[e] = seen ? __uint_as_float(o[e]) * inv : 0.f;
         const int col = (D / 2) * hf + c0;
         if (dirty)  // non-finite values of the checked tiles, where this row sees them
-          for (int j = t_mask * kVT; j <= limit; ++j) {
+          for (int j = kf + t_mask * kVT; j <= limit && j < kf + nt * kVT; ++j) {
             const uint16_t* vr = a.v + (int64_t)(k0 + j) * a.v_sn + (int64_t)g * a.v_sh + col;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -544,6 +552,12 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
               if ((bits & 0x7F80u) == 0x7F80u) f[e] += __uint_as_float(bits << 16);
             }
           }
+        if (a.part_o) {
+          float4* po = reinterpret_cast<float4*>(a.part_o + (((int64_t)split * a.total_q + row) * a.H + h) * D + col);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) po[u] = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
+          continue;
+        }
         uint4* dst = reinterpret_cast<uint4*>(a.out + (row * a.H + h) * D + col);
 #pragma unroll
         for (int v8 = 0; v8 < 4; ++v8) {
@@ -556,8 +570,13 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           dst[v8] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      if (mine && a.lse && hf == 0)
-        a.lse[row * a.H + h] = seen ? (float)(((double)m_ref + log2((double)sum_row)) * kLn2) : -INFINITY;
+      if (mine && hf == 0) {
+        const double z = (double)m_ref + log2((double)sum_row);
+        if (a.part_z)
+          a.part_z[((int64_t)split * a.total_q + row) * a.H + h] = seen ? (float)z : -INFINITY;
+        else if (a.lse)
+          a.lse[row * a.H + h] = seen ? (float)(z * kLn2) : -INFINITY;
+      }
     }
   }
   tc::tc_fence_before();
@@ -574,6 +593,51 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
+}
+
+// Joins the splits of a row, one warp per (query, head):
+// out = sum_s 2^(z_s - Z) o_s, Z = log2 sum_s 2^z_s; rows of no (sound) sequence are left as they are.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const VarArgs a) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t rh = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);  // row * H + head
+  const int64_t n = a.total_q * a.H;
+  if (rh >= n) return;
+  const int row = (int)(rh / a.H);
+  bool owned = false;
+  for (int b = lane; b < a.batch; b += 32) {
+    bool bad;
+    seq_blocks(a, b, &bad);
+    owned |= !bad && row >= a.cu_q[b] && row < a.cu_q[b + 1];
+  }
+  if (!__any_sync(0xffffffffu, owned)) return;
+  float Z = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) Z = fmaxf(Z, a.part_z[s * n + rh]);
+  float acc[D / 32], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float z = a.part_z[s * n + rh];
+    if (z == -INFINITY) continue;  // no key of the split
+    const float w = tc::ex2_approx(z - Z);
+    sum += w;
+    const float* o = a.part_o + (s * n + rh) * D + lane * (D / 32);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] += w * o[e];
+  }
+  const bool seen = Z != -INFINITY;
+  const float inv = seen ? 1.f / sum : 0.f;
+  if (a.out) {
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2) {
+      const __nv_bfloat162 hp = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+      *reinterpret_cast<__nv_bfloat162*>(a.out + rh * D + lane * (D / 32) + e) = hp;
+    }
+  }
+  if (a.lse && lane == 0) a.lse[rh] = seen ? (float)(((double)Z + log2((double)sum)) * kLn2) : -INFINITY;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -629,7 +693,44 @@ kvc_status launch_varlen(dim3 grid, cudaStream_t st, const CUtensorMap (&maps)[3
   const Launch l(grid, dim3(kVBlock), VarSmem<D>::kBytes, st);
   KVC_CUDA_TRY(l.run(prefill_varlen_kernel<D>, maps[0], maps[1], maps[2], a));
   count_launch();
+  if (a.splits == 1) return KVC_OK;
+  const int64_t warps = a.total_q * a.H, per = kJoinThreads / 32;
+  const Launch j(dim3((unsigned)((warps + per - 1) / per)), dim3(kJoinThreads), 0, st);
+  KVC_CUDA_TRY(j.run(prefill_join_kernel<D>, a));
+  count_launch();
   return KVC_OK;
+}
+
+// Blocks of all sequences: at most one that is not full per sequence.
+int64_t varlen_blocks(int nt, int batch, int64_t total_q, int64_t max_q) {
+  const int64_t per = 2 * nt;
+  return std::min(total_q / per + batch, (int64_t)batch * ((max_q + per - 1) / per));
+}
+
+// CTAs that share the keys of a block.  Few rows over many keys (a window's
+// or a small chunk's queries) leave most SMs without a CTA; the splits are
+// chosen by the time of all waves, in key tiles, with kSplitCost for what a CTA
+// and the joining cost beside its tiles.  At most three CTAs per SM come of it,
+// which bounds the workspace.
+constexpr int64_t kSplitCost = 6;
+int varlen_splits(int64_t items, int64_t max_k) {
+  const int64_t sms = num_sms(), tiles = (max_k + kVT - 1) / kVT;
+  auto cost = [&](int64_t n) {
+    return (items * n + sms - 1) / sms * ((tiles + n - 1) / n + kSplitCost) + (n > 1 ? kSplitCost : 0);
+  };
+  int64_t best = 1;
+  for (int64_t n = 2; n <= 64 && n <= tiles && items * n <= 3 * sms; ++n)
+    if (cost(n) < cost(best)) best = n;
+  return (int)best;
+}
+
+bool carve_varlen(int H, int Hkv, int d, int batch, int64_t total_q, int64_t max_q, int64_t max_k, WsCursor* w, VarArgs* a) {
+  a->splits = varlen_splits(varlen_blocks(kVT / (H / Hkv), batch, total_q, max_q) * Hkv, max_k);
+  if (a->splits == 1) return true;
+  const size_t rows = (size_t)a->splits * (size_t)total_q * H;
+  a->part_z = w->take<float>(rows);
+  a->part_o = w->take<float>(rows * d);
+  return w->ok;
 }
 
 }  // namespace
@@ -644,7 +745,10 @@ extern "C" kvc_status kvc_prefill_varlen_workspace_size(int32_t num_heads, int32
   const kvc_status s = check_varlen(num_heads, num_kv_heads, head_dim, batch, total_q, max_seqlen_q, max_seqlen_k);
   if (s != KVC_OK) return s;
   KVC_CHECK_ARG(bytes != nullptr, "bytes must be non-NULL");
-  *bytes = 0;
+  WsCursor w{nullptr, ~size_t(0)};
+  VarArgs a{};
+  carve_varlen(num_heads, num_kv_heads, head_dim, batch, total_q, max_seqlen_q, max_seqlen_k, &w, &a);
+  *bytes = w.off;
   return KVC_OK;
 }
 
@@ -666,7 +770,6 @@ extern "C" kvc_status kvc_prefill_attention_varlen(
     KVC_CHECK_ARG(st >= head_dim && st % 8 == 0 && st < (int64_t(1) << 36),
                   "strides must be multiples of 8 elements, at least head_dim");
   if (total_q == 0) return KVC_OK;  // no row to write
-  if (!encode_fn()) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   VarArgs a{};
   a.v = v;
   a.v_sn = v_stride_n;
@@ -686,17 +789,20 @@ extern "C" kvc_status kvc_prefill_attention_varlen(
   a.out = out;
   a.lse = lse;
   a.err = dev_err;
+  const int64_t blocks = varlen_blocks(a.nt, batch, total_q, max_seqlen_q);
+  if (blocks == 0) return KVC_OK;
+  KVC_CHECK_ARG(blocks * num_kv_heads < (int64_t(1) << 31), "too many query blocks for one call");
+  WsCursor w{static_cast<char*>(ws), ws_bytes};
+  if (!carve_varlen(num_heads, num_kv_heads, head_dim, batch, total_q, max_seqlen_q, max_seqlen_k, &w, &a) ||
+      (a.splits > 1 && (!ws || !aligned(ws, kWsAlign))))
+    return fail(KVC_ERR_WORKSPACE, "prefill workspace missing, too small or not 256-B aligned");
+  if (!encode_fn()) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   CUtensorMap maps[3];
   s = make_map(&maps[0], q, head_dim, num_heads, total_q, q_stride_n, q_stride_h, a.G, a.nt);
   if (s == KVC_OK) s = make_map(&maps[1], k, head_dim, num_kv_heads, total_k, k_stride_n, k_stride_h, 1, kVT);
   if (s == KVC_OK) s = make_map(&maps[2], v, head_dim, num_kv_heads, total_k, v_stride_n, v_stride_h, 1, kVT);
   if (s != KVC_OK) return s;
-  // blocks of all sequences: at most one that is not full per sequence
-  const int64_t per = 2 * a.nt;
-  const int64_t blocks = std::min(total_q / per + batch, (int64_t)batch * ((max_seqlen_q + per - 1) / per));
-  if (blocks == 0) return KVC_OK;
-  KVC_CHECK_ARG(blocks * num_kv_heads < (int64_t(1) << 31), "too many query blocks for one call");
-  const dim3 grid((unsigned)(blocks * num_kv_heads));
+  const dim3 grid((unsigned)(blocks * num_kv_heads * a.splits));
   const cudaStream_t st = (cudaStream_t)stream;
   return head_dim == 128 ? launch_varlen<128>(grid, st, maps, a) : launch_varlen<64>(grid, st, maps, a);
 }

@@ -81,6 +81,12 @@ def _run_prefill(q, k, v, lq, lk, pad=0, **kw):
     ([5, 9], [140, 9], 16, 1, 128),
     ([3, 2], [130, 2], 128, 1, 64),                     # one token per tile
     ([4], [200], 100, 1, 128),
+    ([32], [3000], 8, 2, 128),                          # few rows over many keys: their keys are split over CTAs
+    ([7, 40, 0, 3], [2500, 900, 10, 1], 4, 1, 64),
+    ([1], [5001], 8, 2, 128),
+    ([130], [2100], 5, 1, 128),
+    ([600], [600], 2, 1, 64),
+    ([20, 700], [5, 690], 2, 1, 128),
 ])
 def test_prefill_varlen_matches_the_form(lq, lk, H, Hkv, d):
     rng = np.random.default_rng(sum(lq) * 131 + sum(lk) + H + d)
@@ -110,6 +116,23 @@ def test_prefill_varlen_reference_moves(G, d):
     w_out, w_lse, tol, tol_lse = ref.prefill_varlen(q, k, v, [0, n], [0, n], 1 / math.sqrt(d))
     _close(_np(lse), w_lse, tol_lse, "lse")
     _close(_np(out), w_out, tol, "out")
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_prefill_varlen_split_keys_with_non_finite_values(bad):
+    rng = np.random.default_rng(19)
+    lq, lk, H, d = [40], [2000], 4, 128
+    q, qd = _bf16(rng, 40, H, d)
+    _, kd = _bf16(rng, 2000, 1, d)
+    _, vd = _bf16(rng, 2000, 1, d)
+    assert kvc.prefill_varlen_workspace_size(H, 1, d, 1, 40, 40, 2000) > 0  # split
+    clean, clean_lse = _run_prefill(qd, kd, vd, lq, lk)
+    vd[1980, 0, 7] = bad  # position of query 20
+    out, lse = _run_prefill(qd, kd, vd, lq, lk)
+    assert torch.equal(lse, clean_lse) and torch.equal(out[:20], clean[:20])
+    assert not torch.isfinite(out[20:, :, 7]).any()
+    rest = [c for c in range(d) if c != 7]
+    assert torch.equal(out[:, :, rest], clean[:, :, rest])
 
 
 @pytest.mark.parametrize("n,at,G", [(700, 650, 4), (700, 130, 1), (1200, 1199, 2), (300, 299, 5)])

@@ -106,6 +106,9 @@ def test_prefill_varlen_refusals(clib):
     assert call(mq=-1) == 1 and call(mk=1 << 31) == 1
     assert call(scale=0.0) == 1 and call(scale=float("nan")) == 1
     assert call(st=(516, 128, 256, 128, 256, 128)) == 1 and call(st=(512, 64, 256, 128, 256, 128)) == 1
+    # few rows over many keys use a workspace
+    assert call(mk=8000, tk=9000, ws=None) == 4 and call(mk=8000, tk=9000, nbytes=64) == 4
+    assert call(mk=8000, tk=9000, ws=ctypes.c_void_p(128)) == 4
     assert call(tq=0) == 0  # nothing to do is not an error, and launches nothing
     assert kvc.launch_count() == before
     n = ctypes.c_size_t()
