@@ -5,9 +5,13 @@
 // per KV head, the most recent tokens always kept; every decoding step reads
 // the retained entries and adds one.  StructKV (gist.science 2604.06746)
 // section 2.A: attention accumulated per token ranks the tokens.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "paged.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace kvc {
 namespace {
@@ -126,9 +130,10 @@ __global__ void __launch_bounds__(kAppThreads, 4) append_kernel(const AppArgs a)
 }
 
 // -------------------------------------------------------------------- evict
-// CTA (KV head, sequence).  Keys are the order-preserving uint32 image of the
-// weights (recent entries the largest key, NaN 0), kept in shared memory where
-// they fit.  One entry too many -- every decoding step -- needs the lowest
+// A pair (KV head, sequence) is a CTA, or a cluster of up to 8 where the pairs
+// are few and long, each with a run of the slots.  Keys are the
+// order-preserving uint32 image of the weights (recent entries the largest key,
+// NaN 0), kept in shared memory where they fit.  One entry too many -- every decoding step -- needs the lowest
 // ranked entry only, one reduction.  Otherwise the budget-th largest key T is
 // found by histograms of 2048 equal bins over the range of the keys, then over
 // the bin that holds it, until the bin is one key or is kept whole (weights
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(kAppThreads, 4) append_kernel(const AppArgs a)
 // moves are made by the CTA itself, many by a second kernel over all SMs.
 constexpr uint32_t kRecentKey = 0xFFFFFFFFu;
 constexpr int kEvBins = 2048;
-constexpr int64_t kEvSmemKeys = 48 * 1024;  // keys of a pair held in shared memory (192 KB)
+constexpr int64_t kEvSmemKeys = 48 * 1024;  // keys of a CTA held in shared memory (192 KB)
 constexpr int64_t kEvInline = 32;           // moves a pair's CTA makes itself
 constexpr int64_t kEvSmall = 4096;          // up to here a pair is a CTA of 256 threads, else of 1024
 constexpr int kMvThreads = 256;
@@ -155,7 +160,9 @@ struct EvArgs {
   int32_t* moves;     // [batch*Hkv]: moves of the pair
   int32_t* lists;     // [batch*Hkv][2][max_move]: slots given up, kept slots above the budget
   uint32_t* keys;     // [batch*Hkv][max_len], or nullptr: shared memory
-  int in_place;       // the CTA makes the moves itself
+  int in_place;       // the pair's first CTA makes the moves itself
+  int cluster;        // CTAs per pair
+  int resident;       // the grid runs at once
   int32_t* err;
 };
 
@@ -186,34 +193,47 @@ __device__ __forceinline__ void move_rows(const Paged& c, int b, int g, const in
   }
 }
 
+// What the CTAs of a pair tell one another, each field written once.
+struct EvShare {
+  uint32_t lo, hi;      // smallest key; largest key that is not recent
+  int low_slot, fresh;  // lowest ranked slot; recent entries
+  int bad;              // a page id outside the pool
+  int eq, give, take;   // keys equal to T; slots given up; kept slots above the budget
+};
+
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kPer = kEvBins / kThreads;  // bins per thread
   extern __shared__ uint32_t sm_keys[];
-  __shared__ uint32_t hist[kEvBins];
+  __shared__ uint32_t hist[2][kEvBins];
   __shared__ uint32_t red[3][kWarps];
   __shared__ int cnt[2][kWarps];
-  __shared__ int bad, sh_bin, sh_left, sh_in;
+  __shared__ EvShare sh;
+  __shared__ int sh_bin, sh_left, sh_in;
   pdl_wait();
+  if (a.resident) pdl_trigger();  // the kernel of the moves may be brought in
+  cg::cluster_group cluster = cg::this_cluster();
+  const int cs = a.cluster, me = (int)blockIdx.x % cs;
   const Paged& c = a.c;
-  const int g = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = (int)blockIdx.x / cs, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = c.seq_lens[b], budget = (int)std::min<int64_t>(a.budget, 0x7FFFFFFF);
   const int64_t pair = (int64_t)b * c.Hkv + g;
   int32_t* give = a.lists + pair * 2 * a.max_move;
   int32_t* take = give + a.max_move;
-  if (tid == 0) bad = n < 0 || n > a.max_len;
-  __syncthreads();
+  bool bad = n < 0 || n > a.max_len;
   int n_moves = 0;
-  if (!bad && n > budget) {
-    // ---- the keys, and the lowest ranked entry: lowest key, then highest slot
-    uint32_t* keys = a.keys ? a.keys + pair * a.max_len : sm_keys;
+  if (!bad && n > budget) {  // the same for every CTA of the pair
+    // ---- the keys of this CTA's slots [s0, s1), and the lowest ranked entry
+    // (lowest key, then highest slot)
+    const int seg = ((n + cs - 1) / cs + 31) / 32 * 32, s0 = min(n, me * seg), s1 = min(n, s0 + seg);
+    uint32_t* keys = (a.keys ? a.keys + pair * a.max_len + s0 : sm_keys) - s0;  // indexed by slot
     const int64_t limit = a.recent > 0 ? (int64_t)c.next_pos[b] - a.recent : 0;
     const bool one = n - budget == 1;
     uint32_t lo = kRecentKey, hi = 0u;
     int low_slot = -1, fresh = 0, gone = 0;
 #pragma unroll 4
-    for (int s = tid; s < n; s += kThreads) {
+    for (int s = s0 + tid; s < s1; s += kThreads) {
       const int p = c.page_of(b, s);
       uint32_t key = 0u;
       if (p < 0) {
@@ -230,34 +250,48 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
       }
       if (key == kRecentKey) ++fresh; else hi = max(hi, key);
     }
-    if (gone) bad = 1;
     {
       const uint32_t lo_w = __reduce_min_sync(0xffffffffu, lo);
       const int slot_w = __reduce_max_sync(0xffffffffu, lo == lo_w ? low_slot : -1);
       const uint32_t hi_w = __reduce_max_sync(0xffffffffu, hi);
       const int fresh_w = __reduce_add_sync(0xffffffffu, fresh);
+      const int gone_w = __any_sync(0xffffffffu, gone);
       if (lane == 0) {
         red[0][warp] = lo_w;
         red[1][warp] = (uint32_t)slot_w;
         red[2][warp] = hi_w;
         cnt[0][warp] = fresh_w;
+        cnt[1][warp] = gone_w;
       }
     }
     __syncthreads();
-    lo = red[0][0];
-    hi = red[2][0];
-    fresh = cnt[0][0];
-    low_slot = (int)red[1][0];
-    for (int w = 1; w < kWarps; ++w) {
-      if (red[0][w] < lo || (red[0][w] == lo && (int)red[1][w] > low_slot)) low_slot = (int)red[1][w];
-      lo = min(lo, red[0][w]);
-      hi = max(hi, red[2][w]);
-      fresh += cnt[0][w];
+    if (tid == 0) {
+      EvShare x{red[0][0], red[2][0], (int)red[1][0], cnt[0][0], cnt[1][0], 0, 0, 0};
+      for (int w = 1; w < kWarps; ++w) {
+        if (red[0][w] < x.lo || (red[0][w] == x.lo && (int)red[1][w] > x.low_slot)) x.low_slot = (int)red[1][w];
+        x.lo = min(x.lo, red[0][w]);
+        x.hi = max(x.hi, red[2][w]);
+        x.fresh += cnt[0][w];
+        x.bad |= cnt[1][w];
+      }
+      sh = x;
     }
-    __syncthreads();
+    cluster.sync();
+    lo = kRecentKey;
+    hi = 0u;
+    low_slot = -1;
+    fresh = 0;
+    for (int r = 0; r < cs; ++r) {
+      const EvShare& x = *cluster.map_shared_rank(&sh, r);
+      if (x.lo < lo || (x.lo == lo && x.low_slot > low_slot)) low_slot = x.low_slot;
+      lo = min(lo, x.lo);
+      hi = max(hi, x.hi);
+      fresh += x.fresh;
+      bad |= x.bad != 0;
+    }
     if (!bad && one) {
       if (low_slot < budget) {
-        if (tid == 0) {
+        if (me == 0 && tid == 0) {
           give[0] = low_slot;
           take[0] = budget;
         }
@@ -269,24 +303,31 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
       int left = budget;
       if (fresh < budget) {
         left = budget - fresh;
-        for (;;) {
+        for (int level = 0;; ++level) {
           T = lo;
           if (lo == hi) break;
-          const int bits = 32 - __clz(hi - lo), sh = bits > 11 ? bits - 11 : 0;
-          for (int i = tid; i < kEvBins; i += kThreads) hist[i] = 0u;
+          // two histograms in turn: the other CTAs have read this one's last
+          // use before they passed the last level's barrier
+          uint32_t* h_me = hist[level & 1];
+          const int bits = 32 - __clz(hi - lo), sft = bits > 11 ? bits - 11 : 0;
+          for (int i = tid; i < kEvBins; i += kThreads) h_me[i] = 0u;
           __syncthreads();
 #pragma unroll 4
-          for (int s = tid; s < n; s += kThreads) {
+          for (int s = s0 + tid; s < s1; s += kThreads) {
             const uint32_t key = keys[s];
-            if (key >= lo && key <= hi) atomicAdd(&hist[(key - lo) >> sh], 1u);
+            if (key >= lo && key <= hi) atomicAdd(&h_me[(key - lo) >> sft], 1u);
           }
-          __syncthreads();
-          int h[kPer], sum = 0;  // this thread's bins, from the largest down
+          cluster.sync();
+          int h[kPer], sum = 0;  // this thread's bins over all CTAs, from the largest down
 #pragma unroll
-          for (int u = 0; u < kPer; ++u) {
-            h[u] = (int)hist[kEvBins - 1 - kPer * tid - u];
-            sum += h[u];
+          for (int u = 0; u < kPer; ++u) h[u] = 0;
+          for (int r = 0; r < cs; ++r) {
+            const uint32_t* hr = cluster.map_shared_rank(h_me, r);
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) h[u] += (int)hr[kEvBins - 1 - kPer * tid - u];
           }
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) sum += h[u];
           int inc = sum;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -308,8 +349,8 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
           }
           __syncthreads();
           left = sh_left;
-          lo += (uint32_t)sh_bin << sh;
-          hi = min(hi, lo + ((1u << sh) - 1u));
+          lo += (uint32_t)sh_bin << sft;
+          hi = min(hi, lo + ((1u << sft) - 1u));
           T = lo;
           const bool whole = sh_in == left;
           __syncthreads();
@@ -317,26 +358,31 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
             left = n;
             break;
           }
-          if (sh == 0) break;
+          if (sft == 0) break;
         }
       }
-      // ---- ranks and lists; warp w owns the slots [w * run, (w + 1) * run)
-      const int run = (n + kThreads - 1) / kThreads * 32, s_end = min(n, (warp + 1) * run);
+      // ---- ranks and lists; a warp owns a run of the CTA's slots
+      const int run = (s1 - s0 + kThreads - 1) / kThreads * 32, w0 = min(s1, s0 + warp * run), w1 = min(s1, w0 + run);
       int eq = 0;
-      for (int s = warp * run + lane; s < s_end; s += 32) eq += keys[s] == T;
+      for (int s = w0 + lane; s < w1; s += 32) eq += keys[s] == T;
       eq = __reduce_add_sync(0xffffffffu, eq);
       if (lane == 0) cnt[0][warp] = eq;
       __syncthreads();
-      int eq_before = 0;
-      for (int w = 0; w < warp; ++w) eq_before += cnt[0][w];
-      __syncthreads();
+      int eq_before = 0, eq_all = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) eq_before += cnt[0][w];
+        eq_all += cnt[0][w];
+      }
+      if (tid == 0) sh.eq = eq_all;
+      cluster.sync();
+      for (int r = 0; r < me; ++r) eq_before += cluster.map_shared_rank(&sh, r)->eq;
       int at[2] = {0, 0};  // slots given up and slots taken before this warp's
       for (int phase = 0; phase < 2; ++phase) {
         int rank = eq_before, n_give = at[0], n_take = at[1];
         const unsigned below = (1u << lane) - 1u;
-        for (int s0 = warp * run; s0 < s_end; s0 += 32) {
-          const int s = s0 + lane;
-          const bool in = s < s_end;
+        for (int sw = w0; sw < w1; sw += 32) {
+          const int s = sw + lane;
+          const bool in = s < w1;
           const uint32_t key = in ? keys[s] : 0u;
           const unsigned eqs = __ballot_sync(0xffffffffu, in && key == T);
           const bool kept = in && (key > T || (key == T && rank + __popc(eqs & below) < left));
@@ -356,20 +402,34 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
             cnt[1][warp] = n_take;
           }
           __syncthreads();
-          for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) {
-              at[0] += cnt[0][w];
-              at[1] += cnt[1][w];
+          int all[2] = {0, 0};
+          for (int w = 0; w < kWarps; ++w)
+            for (int k = 0; k < 2; ++k) {
+              if (w < warp) at[k] += cnt[k][w];
+              all[k] += cnt[k][w];
             }
-            n_moves += cnt[1][w];
+          if (tid == 0) {
+            sh.give = all[0];
+            sh.take = all[1];
+          }
+          cluster.sync();
+          for (int r = 0; r < cs; ++r) {
+            const EvShare& x = *cluster.map_shared_rank(&sh, r);
+            if (r < me) {
+              at[0] += x.give;
+              at[1] += x.take;
+            }
+            n_moves += x.take;
           }
         }
       }
     }
-    __syncthreads();
-    if (a.in_place && n_moves > 0) move_rows(c, b, g, give, take, 0, n_moves, tid, kThreads);
+    cluster.sync();  // the lists are written, and nobody reads another CTA's memory any more
+    if (a.in_place && n_moves > 0 && me == 0) move_rows(c, b, g, give, take, 0, n_moves, tid, kThreads);
+  } else {
+    cluster.sync();  // every CTA of the pair has read the length
   }
-  if (tid == 0) {
+  if (me == 0 && tid == 0) {
     if (bad) set_dev_err(a.err, KVC_DEV_ERR_PAGES);
     a.moves[pair] = n_moves;
     // the length of the sequence moves once all its heads have read it
@@ -402,6 +462,18 @@ kvc_status check_evict(const Paged& c, int64_t max_len, int64_t budget) {
   return KVC_OK;
 }
 
+// CTAs per pair: as many as the SMs hold at once (one of 1024 threads each),
+// with at least kEvSmall slots each.  32 pairs of 32768 entries, moves
+// included: 72 us with one CTA, 57 with two, 53 with four, 117 with eight (two
+// waves).
+int evict_cluster(const Paged& c, int64_t max_len) {
+  const int64_t pairs = (int64_t)c.batch * c.Hkv;
+  int cs = 1;
+  while (cs < 8 && pairs * cs * 2 <= num_sms() && max_len >= kEvSmall * cs * 2) cs *= 2;
+  return cs;
+}
+int64_t evict_segment(int64_t max_len, int cs) { return ((max_len + cs - 1) / cs + 31) / 32 * 32; }
+
 // The workspace: counters first (their place depends on the cache alone).
 bool carve_evict(const Paged& c, int64_t max_len, int64_t budget, WsCursor* w, EvArgs* a) {
   const size_t bg = (size_t)c.batch * c.Hkv;
@@ -409,7 +481,9 @@ bool carve_evict(const Paged& c, int64_t max_len, int64_t budget, WsCursor* w, E
   a->tickets = w->take<uint32_t>((size_t)c.batch);
   a->moves = w->take<int32_t>(bg);
   a->lists = w->take<int32_t>(bg * 2 * (size_t)a->max_move);
-  a->keys = max_len > kEvSmemKeys ? w->take<uint32_t>(bg * (size_t)max_len) : nullptr;
+  a->cluster = evict_cluster(c, max_len);
+  a->resident = (int64_t)bg * a->cluster <= num_sms();
+  a->keys = evict_segment(max_len, a->cluster) > kEvSmemKeys ? w->take<uint32_t>(bg * (size_t)max_len) : nullptr;
   return w->ok;
 }
 
@@ -422,8 +496,9 @@ kvc_status launch_evict(const EvArgs& a, cudaStream_t st) {
     return KVC_OK;
   });
   if (s != KVC_OK) return s;
-  const size_t smem = a.keys ? 0 : (size_t)a.max_len * 4;
-  const Launch l(dim3((unsigned)a.c.Hkv, (unsigned)a.c.batch), dim3(kThreads), smem, st);
+  const size_t smem = a.keys ? 0 : (size_t)evict_segment(a.max_len, a.cluster) * 4;
+  Launch l(dim3((unsigned)(a.c.Hkv * a.cluster), (unsigned)a.c.batch), dim3(kThreads), smem, st);
+  if (a.cluster > 1) l.cluster_x((unsigned)a.cluster);
   KVC_CUDA_TRY(l.run(evict_kernel<kThreads>, a));
   count_launch();
   return KVC_OK;

@@ -34,6 +34,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -83,9 +84,14 @@ struct PdSmem {
   static constexpr int kBox = kPdUnit * 128;            // 16 entries x 64 columns (2 KB)
   static constexpr int kMat = (D / 64) * kBox;          // 16 entries of k or v
   static constexpr int kStage = 2 * kMat;
-  static constexpr int kStages = D == 64 ? 6 : G16 ? 2 : 3;
+  // Two stages keep 128 KB per SM on their way (d = 128), which streams as
+  // fast as 192 KB and queues less: with three the first tile took 4.9 us
+  // instead of 3.6, the slowest CTA ended 12 us after the median instead of 3
+  // (128K entries, 40/8 heads: 99.0 us with three, 93.8 with two).
+  static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kRing = kPdWarps * kStages * kStage;
-  static constexpr int kMerge = 2 * kRows * (D + 4) * 4;  // two warps' rows at a time
+  static constexpr int kRow = D + 4;                           // floats per row: output, max, sum
+  static constexpr int kMerge = kPdWarps * kRows * kRow * 4;  // every warp's rows
   static constexpr size_t kBytes = 1024 + (size_t)kRing + kMerge + (kPdMaxBatch + 1) * 4 + 512;
   static_assert(kPdCtasPerSm * (kBytes + 1024) <= 233472, "CTAs per SM");
 };
@@ -158,7 +164,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   constexpr int kRows = L::kRows, kKS = D / 16, kNT = D / 8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* merge = reinterpret_cast<float*>(sm + L::kRing);                       // [2][kRows][D + 4]
+  float* merge = reinterpret_cast<float*>(sm + L::kRing);                       // [warps][kRows][kRow]
   int* first = reinterpret_cast<int*>(sm + L::kRing + L::kMerge);              // [B + 1]: places before sequence b (per head)
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kRing + L::kMerge + (kPdMaxBatch + 2) / 2 * 8);  // [warps][stages]
   int* flags = reinterpret_cast<int*>(full + kPdWarps * L::kStages);           // abort, last, warp totals, warps' bad flags
@@ -435,8 +441,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       ++taken;
       request();
     }
-    // ---- join the four warps: 2 and 3 into 0 and 1, then 1 into 0 (rows of
-    // heads; the lanes of a quad hold the columns of a row)
+    // ---- join the four warps (the lanes of a quad hold the columns of a row)
     if constexpr (!G16) {
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
@@ -445,80 +450,66 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       }
     }
     constexpr int kHalf = G16 ? 2 : 1;
+    __syncthreads();  // the rows of the piece before are read
 #pragma unroll
     for (int hf = 0; hf < kHalf; ++hf) {
       l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
       l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
+      float* r = merge + (warp * kRows + row + 8 * hf) * L::kRow;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) *reinterpret_cast<float2*>(r + 8 * n + col) = make_float2(o[n][2 * hf], o[n][2 * hf + 1]);
+      if ((lane & 3) == 0) {
+        r[D] = m[hf];
+        r[D + 1] = l[hf];
+      }
     }
     if (lane == 0) flags[6 + warp] = bad;
-#pragma unroll 1
-    for (int half = kPdWarps / 2; half >= 1; half >>= 1) {
-      __syncthreads();
-      if (warp >= half && warp < 2 * half) {
-        float* dst = merge + (warp - half) * kRows * (D + 4);
-#pragma unroll
-        for (int hf = 0; hf < kHalf; ++hf) {
-          float* r = dst + (row + 8 * hf) * (D + 4);
-#pragma unroll
-          for (int n = 0; n < kNT; ++n) *reinterpret_cast<float2*>(r + 8 * n + col) = make_float2(o[n][2 * hf], o[n][2 * hf + 1]);
-          if ((lane & 3) == 0) {
-            r[D] = m[hf];
-            r[D + 1] = l[hf];
-          }
-        }
-      }
-      __syncthreads();
-      if (warp < half) {
-        const float* src = merge + warp * kRows * (D + 4);
-#pragma unroll
-        for (int hf = 0; hf < kHalf; ++hf) {
-          const float* r = src + (row + 8 * hf) * (D + 4);
-          const float m2 = r[D], l2 = r[D + 1], M = fmaxf(m[hf], m2);
-          const float f1 = m[hf] == -INFINITY ? 0.f : tc::ex2_approx(m[hf] - M);
-          const float f2 = m2 == -INFINITY ? 0.f : tc::ex2_approx(m2 - M);
-#pragma unroll
-          for (int n = 0; n < kNT; ++n) {
-            const float2 y = *reinterpret_cast<const float2*>(r + 8 * n + col);
-            o[n][2 * hf] = o[n][2 * hf] * f1 + y.x * f2;
-            o[n][2 * hf + 1] = o[n][2 * hf + 1] * f1 + y.y * f2;
-          }
-          l[hf] = l[hf] * f1 + l2 * f2;
-          m[hf] = M;
-        }
-      }
-    }
+    __syncthreads();
     const bool whole = p.t0 == 0 && p.t1 == p.nu;
     const int64_t h0 = (int64_t)p.b * a.H + p.g * G;  // first head of the pair
-    bad = flags[6] | flags[7] | flags[8] | flags[9];
-    if (bad && tid == 0) set_dev_err(a.err, KVC_DEV_ERR_PAGES);
-    if (warp == 0) {
-      const int slot = 2 * run + (p.t0 == 0 ? 1 : 0);
+    // The four rows of a head as one: its result, or (slot >= 0) a piece's
+    // (max, sum, output).  A thread per four columns.
+    auto combine = [&](int64_t slot, bool none) {
+      for (int i = tid; i < G * (D / 4); i += kPdThreads) {
+        const int h = i / (D / 4), c4 = i % (D / 4);
+        const float* r0 = merge + h * L::kRow;
+        float mw[kPdWarps], M = -INFINITY, Ls = 0.f;
 #pragma unroll
-      for (int hf = 0; hf < kHalf; ++hf) {
-        const int h = row + 8 * hf;
-        if (h >= G) continue;
-        float* dst = whole ? a.out + (h0 + h) * D : a.part_o + ((int64_t)slot * G + h) * D;
-        const float f = !whole ? 1.f : bad ? 0.f : 1.f / l[hf];
+        for (int w = 0; w < kPdWarps; ++w) {
+          mw[w] = r0[w * kRows * L::kRow + D];
+          M = fmaxf(M, mw[w]);
+        }
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
-          *reinterpret_cast<float2*>(dst + 8 * n + col) =
-              bad ? make_float2(0.f, 0.f) : make_float2(o[n][2 * hf] * f, o[n][2 * hf + 1] * f);
-        if ((lane & 3) == 0) {
-          if (whole) {
-            const float z = bad ? -INFINITY : m[hf] + log2f(l[hf]);
-            if (a.lse) a.lse[h0 + h] = (float)((double)z * kLn2);
-            if (a.z) a.z[h0 + h] = z;
-          } else {
-            a.part_ml[((int64_t)slot * G + h) * 2] = m[hf];
-            a.part_ml[((int64_t)slot * G + h) * 2 + 1] = bad ? -1.f : l[hf];
-          }
+        for (int w = 0; w < kPdWarps; ++w) {
+          const float* r = r0 + w * kRows * L::kRow;
+          const float f = mw[w] == -INFINITY ? 0.f : tc::ex2_approx(mw[w] - M);
+          const float4 x = *reinterpret_cast<const float4*>(r + 4 * c4);
+          Ls += f * r[D + 1];
+          y.x += f * x.x;
+          y.y += f * x.y;
+          y.z += f * x.z;
+          y.w += f * x.w;
+        }
+        if (slot >= 0) {
+          *reinterpret_cast<float4*>(a.part_o + (slot * G + h) * D + 4 * c4) = y;
+          if (c4 == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * G + h) * 2) = make_float2(M, none ? -1.f : Ls);
+          continue;
+        }
+        const float inv = 1.f / Ls;
+        *reinterpret_cast<float4*>(a.out + (h0 + h) * D + 4 * c4) =
+            none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+        if (c4 == 0) {
+          const float z = none ? -INFINITY : M + log2f(Ls);
+          if (a.lse) a.lse[h0 + h] = (float)((double)z * kLn2);
+          if (a.z) a.z[h0 + h] = z;
         }
       }
-    }
-    if (whole) {
-      __syncthreads();  // the merge rows and flags are free again
-      continue;
-    }
+    };
+    bad = flags[6] | flags[7] | flags[8] | flags[9];
+    if (bad && tid == 0) set_dev_err(a.err, KVC_DEV_ERR_PAGES);
+    combine(whole ? -1 : 2 * run + (p.t0 == 0 ? 1 : 0), bad);
+    if (whole) continue;
     // ---- the last run of the pair joins the pieces
     const int c0 = rs.of(p.pair), c1 = rs.of(p.pair + p.nu - 1);
     __threadfence();
@@ -532,48 +523,77 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     __syncthreads();
     if (!flags[1]) continue;
     __threadfence();
-    for (int h = warp; h < G; h += kPdWarps) {
-      // piece i is slot 1 of run c0 or slot 0 of run c0 + i
-      auto slot_of = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * G + h; };
-      const int np = c1 - c0 + 1;
-      float M = -INFINITY;
-      bool none = false;
-      for (int i = lane; i < np; i += 32) {
-        M = fmaxf(M, __ldcg(a.part_ml + slot_of(i) * 2));
-        none |= __ldcg(a.part_ml + slot_of(i) * 2 + 1) == -1.f;
-      }
+    // Piece i is slot 1 of run c0 or slot 0 of run c0 + i.  The warps share out
+    // the pieces, kIn of them requested at once and a head's while the head
+    // before is worked off; every warp's (max, sum, output) of a head then
+    // goes into the rows in shared memory.
+    const int np = c1 - c0 + 1;
+    constexpr int kIn = 8, kDL = D / 32;
+    using Vec = typename std::conditional<D == 128, float4, float2>::type;
+    bool none = false;
+    float2 ml[2][kIn];
+    Vec y[2][kIn];
+    auto fetch = [&](float2(&mlb)[kIn], Vec(&yb)[kIn], int h, int i0) {
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-      none = __any_sync(0xffffffffu, none);
-      float acc[D / 32], Ls = 0.f;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-#pragma unroll 4
-      for (int i = 0; i < np; ++i) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + slot_of(i) * 2));
-        const float f = ml.x == -INFINITY ? 0.f : tc::ex2_approx(ml.x - M);
-        Ls += f * ml.y;
-        if constexpr (D == 128) {
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot_of(i) * D) + lane);
-          acc[0] += f * y.x;
-          acc[1] += f * y.y;
-          acc[2] += f * y.z;
-          acc[3] += f * y.w;
-        } else {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(a.part_o + slot_of(i) * D) + lane);
-          acc[0] += f * y.x;
-          acc[1] += f * y.y;
+      for (int j = 0; j < kIn; ++j) {
+        const int i = i0 + warp + kPdWarps * j;
+        mlb[j] = make_float2(-INFINITY, 0.f);
+        yb[j] = Vec{};
+        if (i < np) {
+          const int64_t at = (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * G + h;
+          mlb[j] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2));
+          yb[j] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + at * D) + lane);
         }
       }
-      const float inv = 1.f / Ls;
+    };
+    const int batches = (np + kPdWarps * kIn - 1) / (kPdWarps * kIn), steps = G * batches;
+    float M = -INFINITY, Ls = 0.f, acc[kDL];
+    auto step = [&](float2(&mlb)[kIn], Vec(&yb)[kIn], int st) {
+      if (st % batches == 0) {
+        M = -INFINITY;
+        Ls = 0.f;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) a.out[(h0 + h) * D + lane * (D / 32) + e] = none ? 0.f : acc[e] * inv;
-      if (lane == 0) {
-        const float z = none ? -INFINITY : M + log2f(Ls);
-        if (a.lse) a.lse[h0 + h] = (float)((double)z * kLn2);
-        if (a.z) a.z[h0 + h] = z;
+        for (int e = 0; e < kDL; ++e) acc[e] = 0.f;
       }
+      float mx = M;
+#pragma unroll
+      for (int j = 0; j < kIn; ++j) mx = fmaxf(mx, mlb[j].x);
+      const float f0 = M == -INFINITY ? 0.f : tc::ex2_approx(M - mx);
+      M = mx;
+      Ls *= f0;
+#pragma unroll
+      for (int e = 0; e < kDL; ++e) acc[e] *= f0;
+#pragma unroll
+      for (int j = 0; j < kIn; ++j) {
+        const float f = mlb[j].x == -INFINITY ? 0.f : tc::ex2_approx(mlb[j].x - M);
+        none |= mlb[j].y == -1.f;
+        Ls += f * mlb[j].y;
+        const float* v = reinterpret_cast<const float*>(&yb[j]);
+#pragma unroll
+        for (int e = 0; e < kDL; ++e) acc[e] += f * v[e];
+      }
+      if (st % batches == batches - 1) {
+        float* r = merge + (warp * kRows + st / batches) * L::kRow;
+        Vec out{};
+#pragma unroll
+        for (int e = 0; e < kDL; ++e) reinterpret_cast<float*>(&out)[e] = acc[e];
+        *reinterpret_cast<Vec*>(r + lane * kDL) = out;
+        if (lane == 0) {
+          r[D] = M;
+          r[D + 1] = Ls;
+        }
+      }
+    };
+    fetch(ml[0], y[0], 0, 0);
+    for (int st = 0; st < steps; st += 2) {
+      if (st + 1 < steps) fetch(ml[1], y[1], (st + 1) / batches, (st + 1) % batches * kPdWarps * kIn);
+      step(ml[0], y[0], st);
+      if (st + 2 < steps) fetch(ml[0], y[0], (st + 2) / batches, (st + 2) % batches * kPdWarps * kIn);
+      if (st + 1 < steps) step(ml[1], y[1], st + 1);
     }
+    if (lane == 0) flags[6 + warp] = none;
+    __syncthreads();
+    combine(-1, flags[6] | flags[7] | flags[8] | flags[9]);
   }
   if (*abort_flag) {  // a copy never landed: nothing of the stages may be in flight when the CTA leaves
     for (unsigned i = issued > (unsigned)L::kStages ? issued - L::kStages : 0; i < issued; ++i)

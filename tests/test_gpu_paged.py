@@ -533,7 +533,8 @@ def test_append_flags_what_does_not_fit():
 @pytest.mark.parametrize("lens,budget,recent,page", [
     ([5, 17, 16, 0, 1], 4, 2, 16), ([17, 18, 33], 17, 0, 16), ([100, 64, 65, 130], 64, 8, 32),
     ([1025], 1024, 32, 64), ([3000, 1500, 7], 700, 700, 128), ([2100], 1, 1, 256), ([2047, 2049], 2048, 1, 16),
-    ([60000], 2000, 32, 128), ([300], 299, 0, 16), ([4500, 4097], 4096, 16, 32)])
+    ([60000], 2000, 32, 128), ([300], 299, 0, 16), ([4500, 4097], 4096, 16, 32), ([16385, 9000], 16384, 100, 64),
+    ([9001, 12000], 8192, 1000, 32), ([420000], 300, 10, 256)])
 @pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
 def test_evict_matches_the_form(lens, budget, recent, page, kind):
     rng = np.random.default_rng(sum(lens) + budget)
