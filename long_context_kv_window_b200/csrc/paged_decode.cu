@@ -512,10 +512,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     if (whole) continue;
     // ---- the last run of the pair joins the pieces
     const int c0 = rs.of(p.pair), c1 = rs.of(p.pair + p.nu - 1);
-    __threadfence();
     __syncthreads();
     uint32_t* ticket = a.tickets + (int64_t)p.b * Hkv + p.g;
     if (tid == 0) {
+      __threadfence();
       const bool last = atomicAdd(ticket, 1u) == (uint32_t)(c1 - c0);
       if (last) *ticket = 0u;
       flags[1] = last;
@@ -602,30 +602,80 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   }
 }
 
-// weights[j] += sum_h 2^(s_hj - z_h), heads in order: a thread per four entries.
+// weights[j] += sum_h 2^(s_hj - z_h), heads in order: a thread per four
+// entries, 1024 entries of a pair at a time; the CTAs go over the 1024s of all
+// pairs in turn, so short sequences of a ragged batch leave none idle.  What
+// comes before pdl_wait reads only what the decode kernel read too.
 constexpr int kWtThreads = 256;
-__global__ void __launch_bounds__(kWtThreads) paged_weights_kernel(const PdArgs a) {
-  pdl_wait();
+constexpr int kWtSpan = 4 * kWtThreads;
+constexpr int kWtCtasPerSm = 6;
+__global__ void __launch_bounds__(kWtThreads, kWtCtasPerSm) paged_weights_kernel(const PdArgs a) {
+  __shared__ int spans[kPdMaxBatch + 1];  // [b]: spans of the sequences before b (per head)
+  __shared__ int warp_sum[kWtThreads / 32];
   const Paged& c = a.c;
-  const int g = blockIdx.y, b = blockIdx.z;
-  const int n = c.seq_lens[b];
-  const int64_t s = ((int64_t)blockIdx.x * kWtThreads + threadIdx.x) * 4;
-  if (s >= n || n > a.max_len) return;
-  const int64_t h0 = (int64_t)b * a.H + (int64_t)g * a.G;
-  float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int h = 0; h < a.G; ++h) {
-    const float z = __ldg(a.z + h0 + h);
-    if (z == -INFINITY) return;  // a sequence whose pages could not be read
-    const float4 x = *reinterpret_cast<const float4*>(a.logits + (h0 + h) * a.ld + s);
-    w[0] += tc::ex2_approx(x.x - z);
-    w[1] += tc::ex2_approx(x.y - z);
-    w[2] += tc::ex2_approx(x.z - z);
-    w[3] += tc::ex2_approx(x.w - z);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = c.batch;
+  const int per = (B + kWtThreads - 1) / kWtThreads;
+  auto of = [&](int b) {
+    const int n = c.seq_lens[b];
+    return n > 0 && n <= a.max_len ? (n + kWtSpan - 1) / kWtSpan : 0;
+  };
+  int mine = 0;
+  for (int u = 0; u < per; ++u)
+    if (tid * per + u < B) mine += of(tid * per + u);
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
   }
-  float* dst = c.weights + c.entry(c.page_of(b, s), g, s);
-  for (int e = 0; e < 4; ++e)
-    if (s + e < n) dst[e] += w[e];
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int at = inc - mine;
+  for (int w = 0; w < warp; ++w) at += warp_sum[w];
+  for (int u = 0; u < per; ++u) {
+    const int b = tid * per + u;
+    if (b >= B) break;
+    spans[b] = at;
+    at += of(b);
+    if (b == B - 1) spans[B] = at;
+  }
+  __syncthreads();
+  pdl_wait();
+  const int64_t total = (int64_t)spans[B] * c.Hkv;
+  for (int64_t x = blockIdx.x; x < total; x += gridDim.x) {
+    int lo = 0, hi = B - 1;  // the last sequence whose spans begin at or before x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((int64_t)spans[mid] * c.Hkv <= x) lo = mid; else hi = mid - 1;
+    }
+    const int b = lo, mine_n = spans[b + 1] - spans[b];
+    const int r = (int)(x - (int64_t)spans[b] * c.Hkv), g = r / mine_n;
+    const int n = c.seq_lens[b];
+    const int64_t s = (int64_t)(r % mine_n) * kWtSpan + 4 * tid;
+    if (s >= n) continue;
+    const int64_t h0 = (int64_t)b * a.H + (int64_t)g * a.G;
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    bool read = true;
+#pragma unroll 4
+    for (int h = 0; h < a.G; ++h) {
+      const float z = a.z[h0 + h];
+      const float4 y = *reinterpret_cast<const float4*>(a.logits + (h0 + h) * a.ld + s);
+      read &= z != -INFINITY;  // otherwise the sequence's pages could not be read
+      w[0] += tc::ex2_approx(y.x - z);
+      w[1] += tc::ex2_approx(y.y - z);
+      w[2] += tc::ex2_approx(y.z - z);
+      w[3] += tc::ex2_approx(y.w - z);
+    }
+    if (!read) continue;
+    float* dst = c.weights + c.entry(c.page_of(b, s), g, s);
+    if (s + 4 <= n) {
+      float4 old = *reinterpret_cast<float4*>(dst);
+      *reinterpret_cast<float4*>(dst) = make_float4(old.x + w[0], old.y + w[1], old.z + w[2], old.w + w[3]);
+    } else {
+      for (int e = 0; e < 4; ++e)
+        if (s + e < n) dst[e] += w[e];
+    }
+  }
 }
 
 kvc_status check_paged_decode(const Paged& c, int32_t H, int64_t max_len) {
@@ -717,7 +767,8 @@ extern "C" kvc_status kvc_paged_decode_attention(const kvc_paged_cache* c, const
   KVC_CHECK_ARG(q_stride_b >= 0 && q_stride_h >= 0 && q_stride_b % 8 == 0 && q_stride_h % 8 == 0,
                 "strides of q must be multiples of 8 elements");
   KVC_CHECK_ARG(scale > 0.f && scale < 1e30f, "scale must be positive and finite");
-  KVC_CHECK_ARG(!accumulate || a.c.weights, "accumulating needs the cache's weights");
+  KVC_CHECK_ARG(!accumulate || (a.c.weights && aligned(a.c.weights, 16)),
+                "accumulating needs the cache's weights, 16-byte aligned");
   if (!ws || !aligned(ws, kWsAlign)) return fail(KVC_ERR_WORKSPACE, "paged decode workspace missing or not 256-B aligned");
   WsCursor w{static_cast<char*>(ws), ws_bytes};
   if (!carve(a.c, num_heads, max_len, accumulate != 0, &w, &a))
@@ -755,8 +806,8 @@ extern "C" kvc_status kvc_paged_decode_attention(const kvc_paged_cache* c, const
   else
     s = a.G > 8 ? launch_paged_decode<64, true>(runs, st, maps, a) : launch_paged_decode<64, false>(runs, st, maps, a);
   if (s != KVC_OK || !accumulate) return s;
-  const Launch l(dim3((unsigned)((max_len + 4 * kWtThreads - 1) / (4 * kWtThreads)), (unsigned)a.c.Hkv, (unsigned)a.c.batch),
-                 dim3(kWtThreads), 0, st);
+  const int64_t spans = (int64_t)a.c.batch * a.c.Hkv * ((max_len + kWtSpan - 1) / kWtSpan);
+  const Launch l(dim3((unsigned)std::min<int64_t>(spans, (int64_t)kWtCtasPerSm * num_sms())), dim3(kWtThreads), 0, st);
   KVC_CUDA_TRY(l.run(paged_weights_kernel, a));
   count_launch();
   return KVC_OK;
