@@ -17,15 +17,18 @@ namespace kvc {
 namespace {
 
 // ------------------------------------------------------------------- append
-// A copy: per kept entry 2 d bf16 values of k and of v in, the same out, and
-// (weight, position).  CTA (run of kAppRows entries, sequence); its items are
-// 16-byte pieces in the order (piece, head, entry) -- the order in memory of
-// the packed source -- and a thread requests kAppUnroll of them before its
-// first store.  Lengths move on once every CTA has read them: the last CTA of
-// the grid (a ticket counter, returned to zero) adds the new entries.
+// A copy: per kept entry and KV head 2 d bf16 values of k and of v in, the
+// same out, and (weight, position).  A warp takes kAppItems (entry, head)
+// items: one lane each finds its token, half the lanes (or a quarter, d = 64)
+// request an item's k row and as many its v row, all items before the first
+// store, and the lanes of the items find the places meanwhile.  Items go head by head within an entry
+// where the tokens lie so (a whole prompt), entry by entry within a head where
+// a list selects them (the list and the pages then run on).  Lengths move on
+// once every CTA has read them: the last CTA of the grid (a ticket counter,
+// returned to zero) adds the new entries.
 constexpr int kAppThreads = 256;
-constexpr int kAppRows = 8;
-constexpr int kAppUnroll = 4;
+constexpr int kAppItems = 8;  // per warp
+constexpr int kAppSpan = kAppThreads / 32 * kAppItems;
 
 struct AppArgs {
   Paged c;
@@ -59,58 +62,59 @@ __device__ AppSeq app_seq(const AppArgs& a, int b) {
   return s;
 }
 
-__global__ void __launch_bounds__(kAppThreads, 4) append_kernel(const AppArgs a) {
+template <int D>
+__global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a) {
+  constexpr int kPieces = D / 8;             // 16-byte pieces per row
+  constexpr int kAtOnce = 32 / (2 * kPieces);  // items a warp copies per instruction
   __shared__ int last;
   pdl_wait();
-  const int b = blockIdx.y;
+  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Paged& c = a.c;
   const AppSeq q = app_seq(a, b);
-  const int64_t r0 = (int64_t)blockIdx.x * kAppRows;
-  const int rows = (int)(q.kept - r0 < kAppRows ? q.kept - r0 : kAppRows);  // <= 0 past the entries
-  const int log_np = c.d == 128 ? 4 : 3, np = 1 << log_np;                // 16-byte pieces per row
-  const int items = rows * np * c.Hkv;
-  const int64_t npos = c.next_pos ? c.next_pos[b] : 0;
-  for (int i0 = threadIdx.x; i0 < items; i0 += kAppThreads * kAppUnroll) {
-    uint4 kv[kAppUnroll], vv[kAppUnroll];
-    int64_t dst[kAppUnroll];
+  const unsigned kept = (unsigned)q.kept, heads = (unsigned)c.Hkv, items = kept * heads;  // below 2^31
+  const unsigned i0 = blockIdx.x * kAppSpan + warp * kAppItems;
+  if (i0 < items) {
+    // elements from k (and v) to the item's rows; -1: a zero row, nothing
+    int64_t src = -1, dst = -1, t = -1, r = 0;  // t: local token
+    int g = 0;
+    const bool mine = lane < kAppItems && i0 + lane < items;
+    if (mine) {
+      const unsigned i = i0 + lane, by = a.idx ? kept : heads, hi = i / by, lo = i - hi * by;
+      r = a.idx ? lo : hi;
+      g = (int)(a.idx ? hi : lo);
+      t = a.idx ? a.idx[((int64_t)b * c.Hkv + g) * a.kk + r] : r;
+      if (t < 0 || t >= q.len) t = -1;
+      if (t >= 0) src = (q.start + t) * a.sn + (int64_t)g * a.sh;
+    }
+    const int sub = lane / (2 * kPieces), piece = lane % kPieces * 8;
+    const bool value = (lane / kPieces) & 1;
+    const uint16_t* from = value ? a.v : a.k;
+    uint16_t* to = value ? c.v : c.k;
+    uint4 x[kAppItems / kAtOnce];
 #pragma unroll
-    for (int u = 0; u < kAppUnroll; ++u) {
-      const int i = i0 + u * kAppThreads;
-      dst[u] = -1;
-      if (i >= items) continue;
-      const int piece = i & (np - 1), r = (i >> log_np) / c.Hkv, g = (i >> log_np) % c.Hkv;
-      const int64_t slot = q.slot + r0 + r;
-      int64_t t = r0 + r;  // local token
-      if (a.idx) {
-        t = a.idx[((int64_t)b * c.Hkv + g) * a.kk + r0 + r];
-        if (t < 0 || t >= q.len) t = -1;
-      }
+    for (int u = 0; u < kAppItems / kAtOnce; ++u) {
+      const int64_t s = __shfl_sync(0xffffffffu, src, u * kAtOnce + sub);
+      x[u] = s >= 0 ? __ldcs(reinterpret_cast<const uint4*>(from + s + piece)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    // the place, while the rows are on their way
+    if (mine) {
+      const int64_t slot = q.slot + r;
       const int p = c.page_of(b, slot);
+      if (t < 0) set_dev_err(a.err, KVC_DEV_ERR_INDEX);
       if (p < 0) {
         set_dev_err(a.err, KVC_DEV_ERR_PAGES);
-        continue;
-      }
-      kv[u] = vv[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (t >= 0) {
-        const int64_t src = (q.start + t) * a.sn + (int64_t)g * a.sh + piece * 8;
-        kv[u] = __ldcs(reinterpret_cast<const uint4*>(a.k + src));
-        vv[u] = __ldcs(reinterpret_cast<const uint4*>(a.v + src));
       } else {
-        set_dev_err(a.err, KVC_DEV_ERR_INDEX);
-      }
-      dst[u] = c.row(p, g, slot) + piece * 8;
-      if (piece == 0) {
+        dst = c.row(p, g, slot);
         const int64_t e = c.entry(p, g, slot);
-        if (c.pos) c.pos[e] = t >= 0 ? (int32_t)(npos + t) : -1;
+        if (c.pos) c.pos[e] = t >= 0 ? (int32_t)(c.next_pos[b] + t) : -1;
         if (c.weights) c.weights[e] = a.scores && t >= 0 ? a.scores[(int64_t)g * a.total + q.start + t] : 0.f;
       }
     }
 #pragma unroll
-    for (int u = 0; u < kAppUnroll; ++u)
-      if (dst[u] >= 0) {
-        *reinterpret_cast<uint4*>(c.k + dst[u]) = kv[u];
-        *reinterpret_cast<uint4*>(c.v + dst[u]) = vv[u];
-      }
+    for (int u = 0; u < kAppItems / kAtOnce; ++u) {
+      const int64_t d = __shfl_sync(0xffffffffu, dst, u * kAtOnce + sub);
+      if (d >= 0) *reinterpret_cast<uint4*>(to + d + piece) = x[u];
+    }
   }
   __syncthreads();  // every thread has read the lengths
   if (threadIdx.x == 0) {
@@ -549,10 +553,11 @@ extern "C" kvc_status kvc_paged_append(const kvc_paged_cache* c, const uint16_t*
   a.scores = scores;
   a.ticket = static_cast<uint32_t*>(ws);
   a.err = dev_err;
-  const int64_t most = idx ? std::min(kk, max_seqlen) : max_seqlen;
-  const unsigned runs = (unsigned)std::max<int64_t>(1, (most + kAppRows - 1) / kAppRows);
-  const Launch l(dim3(runs, (unsigned)a.c.batch), dim3(kAppThreads), 0, (cudaStream_t)stream);
-  KVC_CUDA_TRY(l.run(append_kernel, a));
+  const int64_t most = (idx ? std::min(kk, max_seqlen) : max_seqlen) * a.c.Hkv;
+  KVC_CHECK_ARG(most < (int64_t(1) << 31), "a sequence's new entries times num_kv_heads must be below 2^31");
+  const int64_t spans = std::max<int64_t>(1, (most + kAppSpan - 1) / kAppSpan);
+  const Launch l(dim3((unsigned)spans, (unsigned)a.c.batch), dim3(kAppThreads), 0, (cudaStream_t)stream);
+  KVC_CUDA_TRY(a.c.d == 128 ? l.run(append_kernel<128>, a) : l.run(append_kernel<64>, a));
   count_launch();
   return KVC_OK;
 }
