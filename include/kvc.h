@@ -383,16 +383,19 @@ kvc_status kvc_prefill_varlen_workspace_size(int32_t num_heads, int32_t num_kv_h
  *  max_seqlen_q, max_seqlen_k  upper bounds of lq and lk (host values)
  *  out   [total_q][H][d] bf16 out, contiguous, 16-byte aligned, or NULL
  *  lse   [total_q][H] fp32 out, contiguous, or NULL
- *  ws    kvc_prefill_varlen_workspace_size(...) bytes, 256-B aligned; one
- *        call at a time per workspace; it need not be zeroed
+ *  ws    kvc_prefill_varlen_workspace_size(...) bytes, 256-B aligned (NULL
+ *        when that is 0: only calls of few rows over many keys, which are
+ *        split over the keys, need any); one call at a time per workspace; it
+ *        need not be zeroed
  *  dev_err  KVC_DEV_ERR_SEQLENS if a sequence's cu_seqlens are malformed or
  *        it is longer than the bounds (its rows are left as they were),
  *        KVC_DEV_ERR_TIMEOUT
  * head_dim in {64, 128}; at most 128 query heads per KV head; q, k, v 16-byte
- * aligned, strides multiples of 8 elements.  Rounding as in
- * kvc_prefill_attention: bf16 operands, fp32 accumulation, the probabilities
- * enter the output contraction as bf16 and are normalised by the sum of those
- * rounded values; the log-sum-exp sums the fp32 probabilities.  Deterministic.
+ * aligned, strides multiples of 8 elements, at least head_dim.  bf16 operands,
+ * fp32 accumulation; the probabilities enter the output contraction as bf16
+ * and the output is normalised by the sum of the fp32 ones, which is the
+ * log-sum-exp's too: |error| <= 2^-8 (mean of |v| under the probabilities) for
+ * the former rounding and as much for the output's.  Deterministic.
  */
 kvc_status kvc_prefill_attention_varlen(const uint16_t* q, int64_t q_stride_n, int64_t q_stride_h, const uint16_t* k,
                                         int64_t k_stride_n, int64_t k_stride_h, const uint16_t* v, int64_t v_stride_n,
@@ -464,7 +467,8 @@ kvc_status kvc_paged_append_workspace_size(const kvc_paged_cache* c, size_t* byt
  *             or a page id is outside the pool (entries in that page are
  *             dropped); KVC_DEV_ERR_INDEX: an idx entry outside [0, len_b)
  *             (a zero row is written, at position -1 with weight 0)
- * The pages written must not be shared by two sequences of the batch.
+ * The pages written must not be shared by two sequences of the batch, nor be
+ * listed twice by one.  A sequence's new entries times Hkv: below 2^31.
  */
 kvc_status kvc_paged_append(const kvc_paged_cache* c, const uint16_t* k, const uint16_t* v, int64_t stride_n,
                             int64_t stride_h, const int32_t* cu_seqlens, int64_t total, int64_t max_seqlen,
@@ -502,7 +506,8 @@ kvc_status kvc_paged_decode_workspace_size(const kvc_paged_cache* c, int32_t num
  *           outside [0, max_len] (that sequence: out = 0, lse = -inf, weights
  *           unchanged); KVC_DEV_ERR_TIMEOUT
  * At most 16 query heads per KV head.  Pages may be shared by sequences
- * unless `accumulate` is set.  fp32 accumulation from the bf16 values; the
+ * unless `accumulate` is set (which also wants the weights 16-byte aligned).
+ * fp32 accumulation from the bf16 values; the
  * probabilities enter the output contraction as a sum of bf16 terms good to
  * ~2^-17 or better.  Deterministic.
  */
@@ -538,7 +543,8 @@ kvc_status kvc_paged_evict_workspace_size(const kvc_paged_cache* c, int64_t max_
  *  dev_err  KVC_DEV_ERR_PAGES: a page id outside the pool or a length outside
  *           [0, max_len] (nothing of that sequence moves, its length stays)
  * Needs weights, and pos and next_pos when recent > 0; pos moves if kept.
- * The pages must not be shared by two sequences of the batch.
+ * The pages must not be shared by two sequences of the batch, nor be listed
+ * twice by one.
  */
 kvc_status kvc_paged_evict(const kvc_paged_cache* c, int64_t max_len, int64_t budget, int64_t recent, void* ws,
                            size_t ws_bytes, int32_t* dev_err, void* stream);

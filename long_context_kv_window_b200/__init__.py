@@ -598,6 +598,12 @@ def _adr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _stride(t: torch.Tensor, dim: int) -> int:
+    """Element stride of a dimension; of one with a single index, which no
+    address depends on, what a dense tensor would have."""
+    return t.stride(dim) if t.shape[dim] > 1 else math.prod(t.shape[dim + 1:])
+
+
 def _raw_stream(stream: Optional[torch.cuda.Stream], dev: torch.device) -> int:
     """_stream as a plain handle, without the stream object of the current stream."""
     if stream is None:
@@ -662,8 +668,8 @@ def kvc_prefill_attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
         need = prefill_varlen_workspace_size(H, Hkv, d, B, total_q, max_seqlen_q, max_seqlen_k)
         ws = _scratch(need, dev, stream) if need else None
     sc = float(1.0 / math.sqrt(d) if scale is None else scale)
-    _check(_call(dev, lib().kvc_prefill_attention_varlen, _adr(q), q.stride(0), q.stride(1), _adr(k), k.stride(0),
-                 k.stride(1), _adr(v), v.stride(0), v.stride(1), _adr(cu_seqlens_q), _adr(cu_seqlens_k), B, total_q,
+    _check(_call(dev, lib().kvc_prefill_attention_varlen, _adr(q), _stride(q, 0), _stride(q, 1), _adr(k),
+                 _stride(k, 0), _stride(k, 1), _adr(v), _stride(v, 0), _stride(v, 1), _adr(cu_seqlens_q), _adr(cu_seqlens_k), B, total_q,
                  total_k, int(max_seqlen_q), int(max_seqlen_k), H, Hkv, d, sc, _adr(out), _adr(lse), _adr(ws),
                  0 if ws is None else _ws_bytes(ws, dev), _adr(dev_err), _raw_stream(stream, dev)),
            "kvc_prefill_attention_varlen")
@@ -746,8 +752,8 @@ class PagedCache:
         need = self._need.get((call, size_args))
         if need is None:
             out = ctypes.c_size_t(0)
-            _check(getattr(lib(), call + "_workspace_size")(self._ref, *size_args, ctypes.byref(out)),
-                   call + "_workspace_size")
+            _check(_call(self.device, getattr(lib(), call + "_workspace_size"), self._ref, *size_args,
+                         ctypes.byref(out)), call + "_workspace_size")
             need = self._need[call, size_args] = max(int(out.value), 1)
         capturing = torch.cuda.is_current_stream_capturing()
         ws = None if capturing else self._ws.get((call, handle))
@@ -799,7 +805,7 @@ def kvc_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seq
     st = _raw_stream(stream, dev)
     if ws is None:
         ws = cache._workspace("kvc_paged_append", (), st, stream)
-    _check(_call(dev, lib().kvc_paged_append, cache._ref, _adr(k), _adr(v), k.stride(0), k.stride(1),
+    _check(_call(dev, lib().kvc_paged_append, cache._ref, _adr(k), _adr(v), _stride(k, 0), _stride(k, 1),
                  _adr(cu_seqlens), total, int(max_seqlen), _adr(idx), kk, _adr(scores), _adr(ws), _ws_bytes(ws, dev),
                  _adr(dev_err), st), "kvc_paged_append")
     return cache
@@ -835,7 +841,7 @@ def kvc_paged_decode_attention(q: torch.Tensor, cache: PagedCache, scale: Option
     if ws is None:
         ws = cache._workspace("kvc_paged_decode", (H, max_len, int(accumulate)), st, stream)
     sc = float(1.0 / math.sqrt(d) if scale is None else scale)
-    _check(_call(dev, lib().kvc_paged_decode_attention, cache._ref, _adr(q), q.stride(0), q.stride(1), H, sc, max_len,
+    _check(_call(dev, lib().kvc_paged_decode_attention, cache._ref, _adr(q), _stride(q, 0), _stride(q, 1), H, sc, max_len,
                  int(accumulate), _adr(out), _adr(lse), _adr(ws), _ws_bytes(ws, dev), _adr(dev_err), st),
            "kvc_paged_decode_attention")
     _used_on(stream, made_out, made_lse)

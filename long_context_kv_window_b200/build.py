@@ -7,8 +7,8 @@ and linked into long_context_kv_window_b200/libkvc.so with the CUDA runtime
 linked statically.  Rebuilds only when a source or header is newer than the
 library.
 
-A second, test-only library libkvc_shortwait.so holds the scoring entry
-points built with a pipeline-wait bound of a few nanoseconds
+A second, test-only library libkvc_shortwait.so holds the scoring, packed
+prefill and paged decode entry points built with a pipeline-wait bound of a few nanoseconds
 (KVC_WAIT_LIMIT_NS): its kernels give up their first wait, record
 KVC_DEV_ERR_TIMEOUT and unwind, which is how the tests exercise the bounded
 waits without a hang.  Nothing but the tests loads it.
@@ -28,7 +28,7 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(CSRC, "_build")
 LIB = os.path.join(PKG, "libkvc.so")
 SHORTWAIT_LIB = os.path.join(PKG, "libkvc_shortwait.so")
-SHORTWAIT_SOURCES = ("score.cu", "api.cu")  # the entry points with pipeline waits, and what they need
+SHORTWAIT_SOURCES = ("score.cu", "prefill_varlen.cu", "paged_decode.cu", "api.cu")  # the entry points with pipeline waits, and what they need
 SHORTWAIT_FLAGS = ["-DKVC_WAIT_LIMIT_NS=1ull"]
 INCLUDE = os.path.join(ROOT, "include")
 

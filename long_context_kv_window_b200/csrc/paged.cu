@@ -532,6 +532,7 @@ extern "C" kvc_status kvc_paged_append(const kvc_paged_cache* c, const uint16_t*
   kvc_status s = check_paged(c, &a.c);
   if (s == KVC_OK) s = check_paged_pointers(a.c);
   if (s != KVC_OK) return s;
+  if (total == 0 && cu_seqlens) return KVC_OK;  // no token to write
   KVC_CHECK_ARG(k && v && aligned(k, 16) && aligned(v, 16), "k and v must be non-NULL and 16-byte aligned");
   KVC_CHECK_ARG(stride_n >= 0 && stride_h >= 0 && stride_n % 8 == 0 && stride_h % 8 == 0,
                 "strides must be multiples of 8 elements");

@@ -470,7 +470,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       if (pass == 1) m_ref = -INFINITY;
       for (int t = 0; t < nt; ++t) {
         if (!tc::mbar_wait(&bars->s_full[i], (ub + t) & 1, abort_flag)) ok = false;
-        if (releases) {  // S(t) is there: K(t) and, before it, V(t - 1) are read
+        if (releases && ok) {  // S(t) is there: K(t) and, before it, V(t - 1) are read
           if (pass == 1) {
             tc::mbar_arrive(&bars->empty[(base + t) % L::kStages]);
           } else {
@@ -513,13 +513,13 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         }
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars->p_full[i]);
+        if (lane == 0 && ok) tc::mbar_arrive(&bars->p_full[i]);
       }
       if (pass == 1) {
         m_ref = both(m_ref, larger);
       } else {
         if (nt > 0 && !tc::mbar_wait(&bars->o_done[i], pass >> 1, abort_flag)) ok = false;
-        if (nt > 0 && releases) tc::mbar_arrive(&bars->empty[(base + 2 * nt - 1) % L::kStages]);
+        if (nt > 0 && releases && ok) tc::mbar_arrive(&bars->empty[(base + 2 * nt - 1) % L::kStages]);
         if (pass == 0 && past && mine) bars->redo = 1;
       }
     }
@@ -761,15 +761,16 @@ extern "C" kvc_status kvc_prefill_attention_varlen(
   clear_error();
   kvc_status s = check_varlen(num_heads, num_kv_heads, head_dim, batch, total_q, max_seqlen_q, max_seqlen_k);
   if (s != KVC_OK) return s;
+  if (total_q == 0) return KVC_OK;  // no row to write
+  KVC_CHECK_ARG(total_k >= 0 && total_k < (int64_t(1) << 31), "need 0 <= total_k < 2^31");
+  if (total_k == 0) k = v = q;  // no key to read: the maps only need an address
   KVC_CHECK_ARG(q && k && v && cu_seqlens_q && cu_seqlens_k, "q, k, v and the cu_seqlens must be non-NULL");
-  KVC_CHECK_ARG(total_k >= 1 && total_k < (int64_t(1) << 31), "need 1 <= total_k < 2^31");
   KVC_CHECK_ARG(scale > 0.f && scale < 1e30f, "scale must be positive and finite");
   KVC_CHECK_ARG(aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && (!out || aligned(out, 16)),
                 "q, k, v and out must be 16-byte aligned");
   for (const int64_t st : {q_stride_n, q_stride_h, k_stride_n, k_stride_h, v_stride_n, v_stride_h})
     KVC_CHECK_ARG(st >= head_dim && st % 8 == 0 && st < (int64_t(1) << 36),
                   "strides must be multiples of 8 elements, at least head_dim");
-  if (total_q == 0) return KVC_OK;  // no row to write
   VarArgs a{};
   a.v = v;
   a.v_sn = v_stride_n;
@@ -799,8 +800,8 @@ extern "C" kvc_status kvc_prefill_attention_varlen(
   if (!encode_fn()) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   CUtensorMap maps[3];
   s = make_map(&maps[0], q, head_dim, num_heads, total_q, q_stride_n, q_stride_h, a.G, a.nt);
-  if (s == KVC_OK) s = make_map(&maps[1], k, head_dim, num_kv_heads, total_k, k_stride_n, k_stride_h, 1, kVT);
-  if (s == KVC_OK) s = make_map(&maps[2], v, head_dim, num_kv_heads, total_k, v_stride_n, v_stride_h, 1, kVT);
+  if (s == KVC_OK) s = make_map(&maps[1], k, head_dim, num_kv_heads, std::max<int64_t>(1, total_k), k_stride_n, k_stride_h, 1, kVT);
+  if (s == KVC_OK) s = make_map(&maps[2], v, head_dim, num_kv_heads, std::max<int64_t>(1, total_k), v_stride_n, v_stride_h, 1, kVT);
   if (s != KVC_OK) return s;
   const dim3 grid((unsigned)(blocks * num_kv_heads * a.splits));
   const cudaStream_t st = (cudaStream_t)stream;

@@ -285,6 +285,35 @@ def test_prefill_varlen_lse_only_and_bad_seqlens():
         assert cu[1] == 30 or torch.equal(out[good], full[good]), cu
 
 
+def test_prefill_varlen_without_keys_or_queries():
+    q = torch.randn(5, 4, 128, device="cuda").bfloat16()
+    none = torch.empty((0, 2, 128), dtype=torch.bfloat16, device="cuda")
+    out, lse = _run_prefill(q, none, none, [2, 3], [0, 0])
+    assert (out == 0).all() and (lse == -math.inf).all()
+    k = torch.randn(4, 2, 128, device="cuda").bfloat16()
+    out, lse = kvc.kvc_prefill_attention_varlen(q[:0], k, k, _dev_i32([0, 0]), _dev_i32([0, 4]), 0, 4)
+    assert out.shape == (0, 4, 128) and lse.shape == (0, 4)
+
+
+def test_one_index_dimensions_may_have_any_stride():
+    """A size-1 token or head dimension whose stride no dense tensor has."""
+    rng = np.random.default_rng(37)
+    q, qd = _bf16(rng, 1, 1, 64)
+    k, kd = _bf16(rng, 9, 1, 64)
+    odd = torch.as_strided(qd, (1, 1, 64), (3, 5, 1))
+    kodd = torch.as_strided(kd, (9, 1, 64), (64, 1, 1))
+    out, lse = _run_prefill(odd, kodd, kodd, [1], [9])
+    w_out, w_lse, tol, tol_lse = ref.prefill_varlen(q, k, k, [0, 1], [0, 9], 0.125)
+    _close(_np(out), w_out, tol, "out")
+    _close(_np(lse), w_lse, tol_lse, "lse")
+    t = Paged(rng, [30], 1, 64, 16, room=4)
+    out, _ = kvc.kvc_paged_decode_attention(odd, t.cache)
+    _close(_np(out), ref.paged_decode(t.pool, q, 0.125)[0], ref.paged_decode(t.pool, q, 0.125)[3], "out")
+    kvc.kvc_paged_append(t.cache, odd, odd, dev_err=t.err)
+    ref.append(t.pool, q, q, [0, 1])
+    t.check_state()
+
+
 # --------------------------------------------------------------------------- #
 # paged cache
 # --------------------------------------------------------------------------- #
@@ -687,3 +716,58 @@ def test_two_streams_and_two_graphs_share_no_workspace():
                 g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+# --------------------------------------------------------------------------- #
+# bounded waits
+# --------------------------------------------------------------------------- #
+def test_wait_bounds_report_a_timeout_and_the_calls_return():
+    """The same kernels with a wait bound of a nanosecond: a wait that would
+    have ended soon gives up, the call records it, lets its copies and MMAs land
+    and returns, and the regular calls after it are right."""
+    import ctypes
+    import os
+
+    from long_context_kv_window_b200 import build as kbuild
+
+    assert os.path.exists(kbuild.SHORTWAIT_LIB), "run `python -m long_context_kv_window_b200.build`"
+    L = ctypes.CDLL(kbuild.SHORTWAIT_LIB)
+    for name in ("kvc_prefill_attention_varlen", "kvc_paged_decode_attention"):
+        fn = getattr(L, name)
+        fn.argtypes, fn.restype = kvc._SIGS[name]
+    rng = np.random.default_rng(81)
+    n, H, Hkv, d = 700, 8, 2, 128
+    q, qd = _bf16(rng, n, H, d)
+    k, kd = _bf16(rng, n, Hkv, d)
+    v, vd = _bf16(rng, n, Hkv, d)
+    cu = _dev_i32([0, n])
+    out, lse = torch.empty_like(qd), torch.empty((n, H), device="cuda")
+    t = Paged(rng, [900, 40], Hkv, d, 16)
+    # a stream long enough that loads queue: 123 MB of entries, pages shared by the sequences
+    pages = torch.randn(15000, Hkv, 16, d, device="cuda").bfloat16()
+    long = kvc.PagedCache(pages, pages, torch.randint(15000, (2, 3750), device="cuda").to(torch.int32),
+                          _dev_i32([60000, 59000]))
+    dq, dout, dlse = qd[:2].contiguous(), torch.empty((2, H, d), device="cuda"), torch.empty((2, H), device="cuda")
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    for _ in range(2):
+        err.zero_()
+        rc = L.kvc_prefill_attention_varlen(qd.data_ptr(), H * d, d, kd.data_ptr(), Hkv * d, d, vd.data_ptr(), Hkv * d, d,
+                                            cu.data_ptr(), cu.data_ptr(), 1, n, n, n, n, H, Hkv, d, 0.1,
+                                            out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), err.data_ptr(), st)
+        torch.cuda.synchronize()
+        assert rc == kvc.KVC_OK and err.item() & kvc.KVC_DEV_ERR_TIMEOUT
+        err.zero_()
+        rc = L.kvc_paged_decode_attention(long._ref, dq.data_ptr(), H * d, d, H, 0.1, long.capacity, 0,
+                                          dout.data_ptr(), dlse.data_ptr(), ws.data_ptr(), ws.numel(), err.data_ptr(), st)
+        torch.cuda.synchronize()
+        assert rc == kvc.KVC_OK
+        if not err.item() & kvc.KVC_DEV_ERR_TIMEOUT:  # every copy was there when it was asked for
+            assert torch.equal(dout, kvc.kvc_paged_decode_attention(dq, long, scale=0.1)[0])
+    out, lse = _run_prefill(qd[:60], kd[:60], vd[:60], [60], [60])
+    w_out, w_lse, tol, tol_lse = ref.prefill_varlen(q[:60], k[:60], v[:60], [0, 60], [0, 60], 1 / math.sqrt(d))
+    _close(_np(out), w_out, tol, "out after the short waits")
+    t.decode(rng, H, True)
+    # the counters went back to zero: the workspace serves on
+    assert torch.equal(kvc.kvc_paged_decode_attention(dq, long, ws=ws)[0], kvc.kvc_paged_decode_attention(dq, long)[0])

@@ -64,6 +64,8 @@ def test_append_refusals(clib):
     assert call(cu=PTR, total=-1) == 1 and call(cu=PTR, total=9, most=-1) == 1
     assert call(cu=PTR, total=9, most=5, idx=PTR, kk=-1) == 1
     assert call(ws=None) == 4 and call(nbytes=16) == 4 and call(ws=ctypes.c_void_p(128)) == 4
+    assert call(cu=PTR, total=9, most=1 << 30, nbytes=256) == 1  # 2^30 entries of two heads
+    assert call(cu=PTR, k=None, total=0, most=0) == 0            # nothing to append
 
 
 def test_decode_refusals(clib):
@@ -102,7 +104,7 @@ def test_prefill_varlen_refusals(clib):
     assert call(q=ctypes.c_void_p(264)) == 1 and call(out=ctypes.c_void_p(264)) == 1
     assert call(d=96) == 2 and call(H=3) == 1 and call(Hkv=0) == 1 and call(H=258) == 2  # 129 heads per KV head
     assert call(B=0) == 1 and call(B=1025) == 1
-    assert call(tq=-1) == 1 and call(tk=0) == 1 and call(tk=1 << 31) == 1
+    assert call(tq=-1) == 1 and call(tk=-1) == 1 and call(tk=1 << 31) == 1
     assert call(mq=-1) == 1 and call(mk=1 << 31) == 1
     assert call(scale=0.0) == 1 and call(scale=float("nan")) == 1
     assert call(st=(516, 128, 256, 128, 256, 128)) == 1 and call(st=(512, 64, 256, 128, 256, 128)) == 1
