@@ -507,9 +507,8 @@ kvc_status kvc_paged_decode_workspace_size(const kvc_paged_cache* c, int32_t num
  *           unchanged); KVC_DEV_ERR_TIMEOUT
  * At most 16 query heads per KV head.  Pages may be shared by sequences
  * unless `accumulate` is set (which also wants the weights 16-byte aligned).
- * fp32 accumulation from the bf16 values; the
- * probabilities enter the output contraction as a sum of bf16 terms good to
- * ~2^-17 or better.  Deterministic.
+ * fp32 accumulation from the bf16 values and the
+ * fp32 probabilities (as three bf16 terms).  Deterministic.
  */
 kvc_status kvc_paged_decode_attention(const kvc_paged_cache* c, const uint16_t* q, int64_t q_stride_b,
                                       int64_t q_stride_h, int32_t num_heads, float scale, int64_t max_len,

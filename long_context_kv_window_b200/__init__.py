@@ -705,9 +705,10 @@ class PagedCache:
         _bf16(v, "v", 4)
         dev = k.device
         num_pages, Hkv, page, d = k.shape
-        if v.shape != k.shape or v.stride() != k.stride():
+        strides = tuple(_stride(k, i) for i in range(4))
+        if v.shape != k.shape or tuple(_stride(v, i) for i in range(4)) != strides:
             raise ValueError("k and v must have the same shape and strides")
-        if k.stride()[1:] != (page * d, d, 1) and k.numel():
+        if strides[1:] != (page * d, d, 1):
             raise ValueError("k and v must be dense within a page, [Hkv][page_size][d]")
         _same_device(dev, v=v, block_table=block_table, seq_lens=seq_lens)
         B = seq_lens.numel()
@@ -727,7 +728,7 @@ class PagedCache:
         self.max_pages = block_table.shape[1]
         self.capacity = self.max_pages * page  # entries per sequence
         adr = [0 if t is None else t.data_ptr() for t in (k, v, weights, pos, block_table, seq_lens, next_pos)]
-        self._c = PagedCacheStruct(*adr, k.stride(0), block_table.stride(0), num_pages, page, self.max_pages, B, Hkv, d)
+        self._c = PagedCacheStruct(*adr, strides[0], _stride(block_table, 0), num_pages, page, self.max_pages, B, Hkv, d)
         self._ref = ctypes.byref(self._c)
         self._ws, self._need = {}, {}
 

@@ -21,9 +21,10 @@
 // logits S[head][entry] (M = 16 heads, the group's and zero rows) come out in
 // the layout in which the second one takes P, so P stays in registers, which
 // the tcgen05 form cannot do; at 4 d bytes per entry the legacy tensor rate is
-// many times what the stream needs.  P enters as two bf16 terms (hi + lo, good
-// to 2^-17); up to 8 heads per group both ride in one MMA, hi in rows 0..7 and
-// lo in rows 8..15.  Row maxima are references that move only when a logit
+// many times what the stream needs.  P enters as three bf16 terms, its 24 bits
+// (two, good to 2^-17, left the output 2.3e-6 off, three 5e-7, in the same
+// time); up to 8 heads per group the first two ride in one MMA, in rows 0..7
+// and 8..15.  Row maxima are references that move only when a logit
 // passes them by more than 8 log2 units (a warp vote; p <= 2^8 otherwise).
 //
 // With `accumulate` the logits go to the workspace (4 G bytes per entry, which
@@ -125,12 +126,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-// (x, y) as bf16 pairs hi + lo
-__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
+// (x, y) as bf16 pairs hi + lo + lo2: the 24 bits of a float, 8 each
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo, uint32_t& lo2) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   const float2 f = __bfloat1622float2(h);
+  x -= f.x;
+  y -= f.y;
+  const __nv_bfloat162 l = __floats2bfloat162_rn(x, y);
+  const float2 e = __bfloat1622float2(l);
   hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = pack_bf16(x - f.x, y - f.y);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+  lo2 = pack_bf16(x - e.x, y - e.y);
 }
 
 // Tiles of a sequence of n entries, per KV head.
@@ -368,16 +374,18 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
         for (int e = 0; e < 2 * kHalf; ++e) {
           const bool valid = 8 * n + col + (e & 1) < left;
-          sc[n][e] = valid ? sc[n][e] * a.c2 : -INFINITY;
+          sc[n][e] = valid ? sc[n][e] : -INFINITY;
           mx[e >> 1] = fmaxf(mx[e >> 1], sc[n][e]);
         }
+      mx[0] *= a.c2;
+      mx[1] *= a.c2;
       if (a.logits) {
 #pragma unroll
         for (int hf = 0; hf < kHalf; ++hf)
           if (row + 8 * hf < G) {
             float* dst = a.logits + ((int64_t)p.b * a.H + p.g * G + row + 8 * hf) * a.ld + s0 + col;
-            *reinterpret_cast<float2*>(dst) = make_float2(sc[0][2 * hf], sc[0][2 * hf + 1]);
-            *reinterpret_cast<float2*>(dst + 8) = make_float2(sc[1][2 * hf], sc[1][2 * hf + 1]);
+            *reinterpret_cast<float2*>(dst) = make_float2(sc[0][2 * hf] * a.c2, sc[0][2 * hf + 1] * a.c2);
+            *reinterpret_cast<float2*>(dst + 8) = make_float2(sc[1][2 * hf] * a.c2, sc[1][2 * hf + 1] * a.c2);
           }
       }
       bool move = mx[0] > m[0] + kPdSlack || (m[0] == -INFINITY && mx[0] > -INFINITY);
@@ -401,15 +409,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[n][e] *= al[e >> 1];
       }
-      uint32_t hi[2][2], lo[2][2];  // [column block][row half]
+      uint32_t hi[2][2], lo[2][2], lo2[2][2];  // [column block][row half]
 #pragma unroll
       for (int hf = 0; hf < kHalf; ++hf) {
         const float ref = m[hf] == -INFINITY ? 0.f : m[hf];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float p0 = tc::ex2_approx(sc[n][2 * hf] - ref), p1 = tc::ex2_approx(sc[n][2 * hf + 1] - ref);
+          const float p0 = tc::ex2_approx(fmaf(sc[n][2 * hf], a.c2, -ref));
+          const float p1 = tc::ex2_approx(fmaf(sc[n][2 * hf + 1], a.c2, -ref));
           l[hf] += p0 + p1;
-          split_bf16(p0, p1, hi[n][hf], lo[n][hf]);
+          split_bf16(p0, p1, hi[n][hf], lo[n][hf], lo2[n][hf]);
         }
       }
 #pragma unroll
@@ -425,8 +434,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           if constexpr (G16) {
             mma_16816(y, hi[0][0], hi[0][1], hi[1][0], hi[1][1], b[2 * u], b[2 * u + 1]);
             mma_16816(y, lo[0][0], lo[0][1], lo[1][0], lo[1][1], b[2 * u], b[2 * u + 1]);
+            mma_16816(y, lo2[0][0], lo2[0][1], lo2[1][0], lo2[1][1], b[2 * u], b[2 * u + 1]);
           } else {
             mma_16816(y, hi[0][0], lo[0][0], hi[1][0], lo[1][0], b[2 * u], b[2 * u + 1]);
+            mma_16816(y, lo2[0][0], 0u, lo2[1][0], 0u, b[2 * u], b[2 * u + 1]);
           }
           float(&on)[4] = o[2 * d16 + u];
           const float2 s01 = tc::add2(make_float2(on[0], on[1]), make_float2(y[0], y[1]));
@@ -470,6 +481,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     // The four rows of a head as one: its result, or (slot >= 0) a piece's
     // (max, sum, output).  A thread per four columns.
     auto combine = [&](int64_t slot, bool none) {
+      bool odd = false;
       for (int i = tid; i < G * (D / 4); i += kPdThreads) {
         const int h = i / (D / 4), c4 = i % (D / 4);
         const float* r0 = merge + h * L::kRow;
@@ -499,12 +511,34 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         const float inv = 1.f / Ls;
         *reinterpret_cast<float4*>(a.out + (h0 + h) * D + 4 * c4) =
             none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+        const float any = (y.x + y.y) + (y.z + y.w);
+        odd |= !none && Ls > 0.f && Ls < INFINITY && !(any - any == 0.f);
         if (c4 == 0) {
           const float z = none ? -INFINITY : M + log2f(Ls);
           if (a.lse) a.lse[h0 + h] = (float)((double)z * kLn2);
           if (a.z) a.z[h0 + h] = z;
         }
       }
+      if (slot >= 0 || !__syncthreads_or(odd)) return;
+      // Sound probabilities and an output that is not finite: entries hold
+      // infinities or NaN in v, and a bf16 term of p that is 0 makes NaN of an
+      // infinity.  The columns that hold them get what sum_j p_j v_j is.
+      int* kinds = reinterpret_cast<int*>(merge);  // per column, 1: +inf, 2: -inf, 4: NaN among the entries
+      for (int i = tid; i < D; i += kPdThreads) kinds[i] = 0;
+      __syncthreads();
+      for (int j = tid; j < p.len; j += kPdThreads) {
+        const uint16_t* vr = c.v + c.row(c.page_of(p.b, j), p.g, j);
+        for (int e = 0; e < D; ++e) {
+          const uint32_t v = vr[e];
+          if ((v & 0x7F80u) == 0x7F80u) atomicOr(&kinds[e], (v & 0x7Fu) ? 4 : (v & 0x8000u) ? 2 : 1);
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < G * D; i += kPdThreads) {
+        const int kind = kinds[i % D];
+        if (kind) a.out[h0 * D + i] = kind == 1 ? INFINITY : kind == 2 ? -INFINITY : __int_as_float(0x7FFFFFFF);
+      }
+      __syncthreads();
     };
     bad = flags[6] | flags[7] | flags[8] | flags[9];
     if (bad && tid == 0) set_dev_err(a.err, KVC_DEV_ERR_PAGES);

@@ -15,7 +15,7 @@ most 2 E + 2^-20 of itself.  The sums over keys add at most 2^-20 (pairwise and
 tiled sums of positive terms).  With A = sum_j p_j |v_j| (the size of the
 terms of an output):
     prefill:  |out - ref| <= (2^-8 + 2 E + 2^-19) A + 2^-8 |out|   (P and out rounded to bf16; |out| <= 1.01 A)
-    decode:   |out - ref| <= (2^-17 + 2 E + 2^-19) A               (P as bf16 terms good to 2^-17)
+    decode:   |out - ref| <= (2^-23 + 2 E + 2^-19) A               (P as three bf16 terms: 24 bits)
     lse:      |lse - ref| <= E + 2^-20 + 2^-23 |lse|
     weights:  |w - ref|   <= (2 E + 2^-19) sum_h p + 2^-24 G |w|
 E is taken as its largest value over the keys of a row.
@@ -108,7 +108,7 @@ def paged_decode(pool: Pool, q, scale):
             for h in range(g * G, (g + 1) * G):
                 r = attend(q[b, h], k, v, scale)
                 out[b, h], lse[b, h] = r.out, r.lse
-                tol[b, h] = (2.0 ** -17 + 2 * r.E + 2.0 ** -19) * r.size
+                tol[b, h] = (2.0 ** -23 + 2 * r.E + 2.0 ** -19) * r.size
                 tol_lse[b, h] = r.E + 2.0 ** -20 + (2.0 ** -23 * abs(r.lse) if n else 0.0)
                 w += r.p
                 tw += (2 * r.E + 2.0 ** -19) * r.p

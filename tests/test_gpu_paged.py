@@ -418,6 +418,30 @@ def test_paged_decode_ignores_what_lies_behind_the_entries(tail):
         Paged(rng, lens, 2, 128, page, tail=tail).decode(rng, 8, True)
 
 
+@pytest.mark.parametrize("lens", [[40], [3000], [70, 900]])
+def test_paged_decode_non_finite_entries(lens):
+    """Values: an infinity or NaN among the entries is what the output's column
+    becomes, and the other columns stay.  A NaN key makes the row NaN."""
+    rng = np.random.default_rng(sum(lens))
+    t = Paged(rng, lens, 2, 128, 16)
+    _, q = _bf16(rng, len(lens), 8, 128)
+    clean, lse = (x.clone() for x in kvc.kvc_paged_decode_attention(q, t.cache))
+    for e, at, x in ((3, 7, math.inf), (9, 39, -math.inf), (12, 0, math.nan), (30, 5, math.inf), (30, 6, -math.inf)):
+        page, g, slot = t.pool.at(0, 1, at)
+        t.cache.v[int(page), g, int(slot), e] = x
+    out, lse2 = kvc.kvc_paged_decode_attention(q, t.cache)
+    assert torch.equal(lse, lse2)
+    hit = out[0, 4:]
+    assert (hit[:, 3] == math.inf).all() and (hit[:, 9] == -math.inf).all() and hit[:, [12, 30]].isnan().all()
+    keep = [e for e in range(128) if e not in (3, 9, 12, 30)]
+    assert torch.equal(hit[:, keep], clean[0, 4:][:, keep]) and torch.equal(out[0, :4], clean[0, :4])
+    assert torch.equal(out[1:], clean[1:])
+    page, g, slot = t.pool.at(0, 0, 11)
+    t.cache.k[int(page), g, int(slot), 2] = math.nan
+    out, lse2 = kvc.kvc_paged_decode_attention(q, t.cache)
+    assert out[0, :4].isnan().all() and lse2[0, :4].isnan().all() and torch.equal(lse2[0, 4:], lse[0, 4:])
+
+
 def test_paged_decode_views_and_bounds():
     """A fused pool (page stride of two pages), strided queries, a tight max_len."""
     rng = np.random.default_rng(9)

@@ -142,6 +142,9 @@ def test_paged_cache_checks_its_tensors(lib):
     assert c.capacity == 48 and c._c.page_stride == 2 * 16 * 64 and c._c.table_stride == 3
     both = torch.empty((6, 2, 2, 16, 64), dtype=bf)
     assert kvc.PagedCache(**{**ok, "k": both[:, 0], "v": both[:, 1]})._c.page_stride == 4 * 16 * 64
+    one = torch.empty((6, 16, 1, 64), dtype=bf).transpose(1, 2)  # one head: its stride is not a dense tensor's
+    heads1 = {n: torch.zeros((6, 1, 16), dtype=t) for n, t in (("weights", f32), ("pos", i32))}
+    assert kvc.PagedCache(**{**ok, **heads1, "k": one, "v": one})._c.page_stride == 16 * 64
     wide = torch.zeros((2, 9), dtype=i32)
     assert kvc.PagedCache(**{**ok, "block_table": wide[:, :3]})._c.table_stride == 9
     for b in (dict(k=torch.empty((6, 2, 16, 64), dtype=f32)), dict(v=torch.empty((6, 2, 16, 128), dtype=bf)),
