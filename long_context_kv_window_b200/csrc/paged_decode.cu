@@ -562,7 +562,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     // before is worked off; every warp's (max, sum, output) of a head then
     // goes into the rows in shared memory.
     const int np = c1 - c0 + 1;
-    constexpr int kIn = 8, kDL = D / 32;
+    constexpr int kIn = 5, kDL = D / 32;
     using Vec = typename std::conditional<D == 128, float4, float2>::type;
     bool none = false;
     float2 ml[2][kIn];
