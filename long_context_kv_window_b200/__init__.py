@@ -779,11 +779,13 @@ def kvc_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seq
     them); with idx int32 [B][Hkv][kk] (kvc_select_topk_varlen's) only the
     selected ones of each KV head.  scores fp32 [Hkv][total] are the entries'
     first weights.  Lengths and positions move on, on the device."""
-    dev = _kv_pair(k, v)
+    dev = cache.device
     if v is None:
         raise ValueError("v is missing")
-    _same_device(cache.device, k=k)
+    _kv_pair(k, v)
     total, Hkv, d = k.shape
+    if k.device != dev:
+        raise ValueError(f"k is on {k.device}, the cache on {dev}")
     if Hkv != cache.num_kv_heads or d != cache.head_dim:
         raise ValueError(f"k and v must be [total][{cache.num_kv_heads}][{cache.head_dim}], got {tuple(k.shape)}")
     if cu_seqlens is None:

@@ -219,6 +219,9 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
   if (a.resident) pdl_trigger();  // the kernel of the moves may be brought in
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = a.cluster, me = (int)blockIdx.x % cs;
+  auto sync_pair = [&] {  // the CTAs of a pair
+    if (cs > 1) cluster.sync(); else __syncthreads();
+  };
   const Paged& c = a.c;
   const int g = (int)blockIdx.x / cs, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = c.seq_lens[b], budget = (int)std::min<int64_t>(a.budget, 0x7FFFFFFF);
@@ -233,7 +236,24 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
     const int seg = ((n + cs - 1) / cs + 31) / 32 * 32, s0 = min(n, me * seg), s1 = min(n, s0 + seg);
     uint32_t* keys = (a.keys ? a.keys + pair * a.max_len + s0 : sm_keys) - s0;  // indexed by slot
     const int64_t limit = a.recent > 0 ? (int64_t)c.next_pos[b] - a.recent : 0;
+    // One entry too many: the only slot above the budget is the one that moves,
+    // if any does, so its row is on its way while the keys are looked at.
     const bool one = n - budget == 1;
+    const int np = c.d / 8;
+    uint4 held = make_uint4(0u, 0u, 0u, 0u);
+    float held_w = 0.f;
+    int held_pos = 0;
+    if (one && me == 0 && tid < 2 * np) {
+      const int p = c.page_of(b, budget);
+      if (p >= 0) {
+        held = *reinterpret_cast<const uint4*>((tid < np ? c.k : c.v) + c.row(p, g, budget) + tid % np * 8);
+        if (tid == 0) {
+          const int64_t e = c.entry(p, g, budget);
+          held_w = c.weights[e];
+          if (c.pos) held_pos = c.pos[e];
+        }
+      }
+    }
     uint32_t lo = kRecentKey, hi = 0u;
     int low_slot = -1, fresh = 0, gone = 0;
 #pragma unroll 4
@@ -280,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
       }
       sh = x;
     }
-    cluster.sync();
+    sync_pair();
     lo = kRecentKey;
     hi = 0u;
     low_slot = -1;
@@ -294,12 +314,14 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
       bad |= x.bad != 0;
     }
     if (!bad && one) {
-      if (low_slot < budget) {
-        if (me == 0 && tid == 0) {
-          give[0] = low_slot;
-          take[0] = budget;
+      if (low_slot < budget && me == 0 && tid < 2 * np) {
+        const int p = c.page_of(b, low_slot);
+        *reinterpret_cast<uint4*>((tid < np ? c.k : c.v) + c.row(p, g, low_slot) + tid % np * 8) = held;
+        if (tid == 0) {
+          const int64_t e = c.entry(p, g, low_slot);
+          c.weights[e] = held_w;
+          if (c.pos) c.pos[e] = held_pos;
         }
-        n_moves = 1;
       }
     } else if (!bad) {
       // ---- T: `left` of the keys equal to T are kept, the lowest slots
@@ -321,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
             const uint32_t key = keys[s];
             if (key >= lo && key <= hi) atomicAdd(&h_me[(key - lo) >> sft], 1u);
           }
-          cluster.sync();
+          sync_pair();
           int h[kPer], sum = 0;  // this thread's bins over all CTAs, from the largest down
 #pragma unroll
           for (int u = 0; u < kPer; ++u) h[u] = 0;
@@ -378,7 +400,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
         eq_all += cnt[0][w];
       }
       if (tid == 0) sh.eq = eq_all;
-      cluster.sync();
+      sync_pair();
       for (int r = 0; r < me; ++r) eq_before += cluster.map_shared_rank(&sh, r)->eq;
       int at[2] = {0, 0};  // slots given up and slots taken before this warp's
       for (int phase = 0; phase < 2; ++phase) {
@@ -416,7 +438,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
             sh.give = all[0];
             sh.take = all[1];
           }
-          cluster.sync();
+          sync_pair();
           for (int r = 0; r < cs; ++r) {
             const EvShare& x = *cluster.map_shared_rank(&sh, r);
             if (r < me) {
@@ -428,10 +450,10 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
         }
       }
     }
-    cluster.sync();  // the lists are written, and nobody reads another CTA's memory any more
+    sync_pair();  // the lists are written, and nobody reads another CTA's memory any more
     if (a.in_place && n_moves > 0 && me == 0) move_rows(c, b, g, give, take, 0, n_moves, tid, kThreads);
   } else {
-    cluster.sync();  // every CTA of the pair has read the length
+    sync_pair();  // every CTA of the pair has read the length
   }
   if (me == 0 && tid == 0) {
     if (bad) set_dev_err(a.err, KVC_DEV_ERR_PAGES);
