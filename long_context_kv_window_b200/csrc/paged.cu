@@ -17,8 +17,8 @@ namespace kvc {
 namespace {
 
 // ------------------------------------------------------------------- append
-// A copy: per kept entry and KV head 2 d bf16 values of k and of v in, the
-// same out, and (weight, position).  A warp takes kAppItems (entry, head)
+// A copy: per kept entry and KV head d bf16 values of k and of v in, the same
+// out, and (weight, position).  A warp takes kRowItems (entry, head)
 // items: one lane each finds its token, half the lanes (or a quarter, d = 64)
 // request an item's k row and as many its v row, all items before the first
 // store, and the lanes of the items find the places meanwhile.  Items go head by head within an entry
@@ -27,8 +27,33 @@ namespace {
 // once every CTA has read them: the last CTA of the grid (a ticket counter,
 // returned to zero) adds the new entries.
 constexpr int kAppThreads = 256;
-constexpr int kAppItems = 8;  // per warp
-constexpr int kAppSpan = kAppThreads / 32 * kAppItems;
+
+// A warp copies up to kRowItems items, lane i < kRowItems holding item i's
+// place in the source (elements; -1: a zero row) and, once found(), in the
+// destination (-1: nothing is written).
+constexpr int kRowItems = 8;
+template <int D, class F>
+__device__ __forceinline__ void copy_rows(const uint16_t* ks, const uint16_t* vs, uint16_t* kd, uint16_t* vd, int64_t src,
+                                          F&& found) {
+  constexpr int kPieces = D / 8;             // 16-byte pieces per row
+  constexpr int kAtOnce = 32 / (2 * kPieces);  // items per instruction
+  const int lane = threadIdx.x & 31, sub = lane / (2 * kPieces), piece = lane % kPieces * 8;
+  const bool value = (lane / kPieces) & 1;
+  const uint16_t* from = value ? vs : ks;
+  uint16_t* to = value ? vd : kd;
+  uint4 x[kRowItems / kAtOnce];
+#pragma unroll
+  for (int u = 0; u < kRowItems / kAtOnce; ++u) {
+    const int64_t s = __shfl_sync(0xffffffffu, src, u * kAtOnce + sub);
+    x[u] = s >= 0 ? __ldcs(reinterpret_cast<const uint4*>(from + s + piece)) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  const int64_t dst = found();  // while the rows are on their way
+#pragma unroll
+  for (int u = 0; u < kRowItems / kAtOnce; ++u) {
+    const int64_t d = __shfl_sync(0xffffffffu, dst, u * kAtOnce + sub);
+    if (d >= 0) *reinterpret_cast<uint4*>(to + d + piece) = x[u];
+  }
+}
 
 struct AppArgs {
   Paged c;
@@ -62,22 +87,20 @@ __device__ AppSeq app_seq(const AppArgs& a, int b) {
   return s;
 }
 
+constexpr int kAppSpan = kAppThreads / 32 * kRowItems;
 template <int D>
 __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a) {
-  constexpr int kPieces = D / 8;             // 16-byte pieces per row
-  constexpr int kAtOnce = 32 / (2 * kPieces);  // items a warp copies per instruction
   __shared__ int last;
   pdl_wait();
   const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Paged& c = a.c;
   const AppSeq q = app_seq(a, b);
   const unsigned kept = (unsigned)q.kept, heads = (unsigned)c.Hkv, items = kept * heads;  // below 2^31
-  const unsigned i0 = blockIdx.x * kAppSpan + warp * kAppItems;
+  const unsigned i0 = blockIdx.x * kAppSpan + warp * kRowItems;
   if (i0 < items) {
-    // elements from k (and v) to the item's rows; -1: a zero row, nothing
-    int64_t src = -1, dst = -1, t = -1, r = 0;  // t: local token
+    int64_t src = -1, t = -1, r = 0;  // t: local token
     int g = 0;
-    const bool mine = lane < kAppItems && i0 + lane < items;
+    const bool mine = lane < kRowItems && i0 + lane < items;
     if (mine) {
       const unsigned i = i0 + lane, by = a.idx ? kept : heads, hi = i / by, lo = i - hi * by;
       r = a.idx ? lo : hi;
@@ -86,35 +109,20 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a) {
       if (t < 0 || t >= q.len) t = -1;
       if (t >= 0) src = (q.start + t) * a.sn + (int64_t)g * a.sh;
     }
-    const int sub = lane / (2 * kPieces), piece = lane % kPieces * 8;
-    const bool value = (lane / kPieces) & 1;
-    const uint16_t* from = value ? a.v : a.k;
-    uint16_t* to = value ? c.v : c.k;
-    uint4 x[kAppItems / kAtOnce];
-#pragma unroll
-    for (int u = 0; u < kAppItems / kAtOnce; ++u) {
-      const int64_t s = __shfl_sync(0xffffffffu, src, u * kAtOnce + sub);
-      x[u] = s >= 0 ? __ldcs(reinterpret_cast<const uint4*>(from + s + piece)) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    // the place, while the rows are on their way
-    if (mine) {
+    copy_rows<D>(a.k, a.v, c.k, c.v, src, [&]() -> int64_t {
+      if (!mine) return -1;
       const int64_t slot = q.slot + r;
       const int p = c.page_of(b, slot);
       if (t < 0) set_dev_err(a.err, KVC_DEV_ERR_INDEX);
       if (p < 0) {
         set_dev_err(a.err, KVC_DEV_ERR_PAGES);
-      } else {
-        dst = c.row(p, g, slot);
-        const int64_t e = c.entry(p, g, slot);
-        if (c.pos) c.pos[e] = t >= 0 ? (int32_t)(c.next_pos[b] + t) : -1;
-        if (c.weights) c.weights[e] = a.scores && t >= 0 ? a.scores[(int64_t)g * a.total + q.start + t] : 0.f;
+        return -1;
       }
-    }
-#pragma unroll
-    for (int u = 0; u < kAppItems / kAtOnce; ++u) {
-      const int64_t d = __shfl_sync(0xffffffffu, dst, u * kAtOnce + sub);
-      if (d >= 0) *reinterpret_cast<uint4*>(to + d + piece) = x[u];
-    }
+      const int64_t e = c.entry(p, g, slot);
+      if (c.pos) c.pos[e] = t >= 0 ? (int32_t)(c.next_pos[b] + t) : -1;
+      if (c.weights) c.weights[e] = a.scores && t >= 0 ? a.scores[(int64_t)g * a.total + q.start + t] : 0.f;
+      return c.row(p, g, slot);
+    });
   }
   __syncthreads();  // every thread has read the lengths
   if (threadIdx.x == 0) {
@@ -151,10 +159,10 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a) {
 constexpr uint32_t kRecentKey = 0xFFFFFFFFu;
 constexpr int kEvBins = 2048;
 constexpr int64_t kEvSmemKeys = 48 * 1024;  // keys of a CTA held in shared memory (192 KB)
-constexpr int64_t kEvInline = 32;           // moves a pair's CTA makes itself
+constexpr int64_t kEvInline = 64;           // moves a pair's CTA makes itself: one per warp and item of 256 threads
 constexpr int64_t kEvSmall = 4096;          // up to here a pair is a CTA of 256 threads, else of 1024
 constexpr int kMvThreads = 256;
-constexpr int kMvRows = 32;                 // moves per CTA of the second kernel and round
+constexpr int kMvSpan = kMvThreads / 32 * kRowItems;  // moves per CTA of the second kernel
 
 struct EvArgs {
   Paged c;
@@ -176,25 +184,28 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Moves i0, i0 + step, ... of a pair's list: 16-byte pieces, weight, position.
+// Moves [i0, i0 + kRowItems) of a pair's n, by one warp.
+template <int D>
 __device__ __forceinline__ void move_rows(const Paged& c, int b, int g, const int32_t* give, const int32_t* take, int i0,
-                                          int i1, int tid, int threads) {
-  const int np = c.d / 8;
-#pragma unroll 4
-  for (int i = i0 * np + tid; i < i1 * np; i += threads) {
-    const int m = i / np, piece = i % np;
-    const int64_t from = take[m], to = give[m];
-    const int pf = c.page_of(b, from), pt = c.page_of(b, to);
-    const int64_t src = c.row(pf, g, from) + piece * 8, dst = c.row(pt, g, to) + piece * 8;
-    const uint4 kv = *reinterpret_cast<const uint4*>(c.k + src), vv = *reinterpret_cast<const uint4*>(c.v + src);
-    *reinterpret_cast<uint4*>(c.k + dst) = kv;
-    *reinterpret_cast<uint4*>(c.v + dst) = vv;
-    if (piece == 0) {
-      const int64_t ef = c.entry(pf, g, from), et = c.entry(pt, g, to);
-      c.weights[et] = c.weights[ef];
-      if (c.pos) c.pos[et] = c.pos[ef];
-    }
+                                          int n) {
+  const int lane = threadIdx.x & 31;
+  const bool mine = lane < kRowItems && i0 + lane < n;
+  int64_t from = 0, src = -1;
+  int pf = 0;
+  if (mine) {
+    from = take[i0 + lane];
+    pf = c.page_of(b, from);
+    src = c.row(pf, g, from);
   }
+  copy_rows<D>(c.k, c.v, c.k, c.v, src, [&]() -> int64_t {
+    if (!mine) return -1;
+    const int64_t to = give[i0 + lane], ef = c.entry(pf, g, from);
+    const int pt = c.page_of(b, to);
+    const int64_t et = c.entry(pt, g, to);
+    c.weights[et] = c.weights[ef];
+    if (c.pos) c.pos[et] = c.pos[ef];
+    return c.row(pt, g, to);
+  });
 }
 
 // What the CTAs of a pair tell one another, each field written once.
@@ -289,16 +300,14 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
       }
     }
     __syncthreads();
-    if (tid == 0) {
-      EvShare x{red[0][0], red[2][0], (int)red[1][0], cnt[0][0], cnt[1][0], 0, 0, 0};
-      for (int w = 1; w < kWarps; ++w) {
-        if (red[0][w] < x.lo || (red[0][w] == x.lo && (int)red[1][w] > x.low_slot)) x.low_slot = (int)red[1][w];
-        x.lo = min(x.lo, red[0][w]);
-        x.hi = max(x.hi, red[2][w]);
-        x.fresh += cnt[0][w];
-        x.bad |= cnt[1][w];
-      }
-      sh = x;
+    if (warp == 0) {
+      const bool in = lane < kWarps;
+      const uint32_t lo_w = in ? red[0][lane] : kRecentKey, lo_c = __reduce_min_sync(0xffffffffu, lo_w);
+      const int slot_c = __reduce_max_sync(0xffffffffu, in && lo_w == lo_c ? (int)red[1][lane] : -1);
+      const uint32_t hi_c = __reduce_max_sync(0xffffffffu, in ? red[2][lane] : 0u);
+      const int fresh_c = __reduce_add_sync(0xffffffffu, in ? cnt[0][lane] : 0);
+      const int bad_c = __any_sync(0xffffffffu, in && cnt[1][lane]);
+      if (lane == 0) sh = EvShare{lo_c, hi_c, slot_c, fresh_c, bad_c, 0, 0, 0};
     }
     sync_pair();
     lo = kRecentKey;
@@ -389,19 +398,21 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
       }
       // ---- ranks and lists; a warp owns a run of the CTA's slots
       const int run = (s1 - s0 + kThreads - 1) / kThreads * 32, w0 = min(s1, s0 + warp * run), w1 = min(s1, w0 + run);
-      int eq = 0;
-      for (int s = w0 + lane; s < w1; s += 32) eq += keys[s] == T;
-      eq = __reduce_add_sync(0xffffffffu, eq);
-      if (lane == 0) cnt[0][warp] = eq;
-      __syncthreads();
-      int eq_before = 0, eq_all = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) eq_before += cnt[0][w];
-        eq_all += cnt[0][w];
+      int eq_before = 0;  // keys equal to T before this warp's slots (not needed where all are kept)
+      if (left < n) {
+        int eq = 0, eq_all = 0;
+        for (int s = w0 + lane; s < w1; s += 32) eq += keys[s] == T;
+        eq = __reduce_add_sync(0xffffffffu, eq);
+        if (lane == 0) cnt[0][warp] = eq;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) eq_before += cnt[0][w];
+          eq_all += cnt[0][w];
+        }
+        if (tid == 0) sh.eq = eq_all;
+        sync_pair();
+        for (int r = 0; r < me; ++r) eq_before += cluster.map_shared_rank(&sh, r)->eq;
       }
-      if (tid == 0) sh.eq = eq_all;
-      sync_pair();
-      for (int r = 0; r < me; ++r) eq_before += cluster.map_shared_rank(&sh, r)->eq;
       int at[2] = {0, 0};  // slots given up and slots taken before this warp's
       for (int phase = 0; phase < 2; ++phase) {
         int rank = eq_before, n_give = at[0], n_take = at[1];
@@ -451,7 +462,12 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
       }
     }
     sync_pair();  // the lists are written, and nobody reads another CTA's memory any more
-    if (a.in_place && n_moves > 0 && me == 0) move_rows(c, b, g, give, take, 0, n_moves, tid, kThreads);
+    if (a.in_place && me == 0 && warp * kRowItems < n_moves) {
+      if (c.d == 128)
+        move_rows<128>(c, b, g, give, take, warp * kRowItems, n_moves);
+      else
+        move_rows<64>(c, b, g, give, take, warp * kRowItems, n_moves);
+    }
   } else {
     sync_pair();  // every CTA of the pair has read the length
   }
@@ -467,15 +483,16 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvArgs a) {
   }
 }
 
-// CTA (round of moves, KV head, sequence)
+// CTA (span of moves, KV head, sequence), a warp per kRowItems of them.
+template <int D>
 __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const EvArgs a) {
   pdl_wait();
   const int g = blockIdx.y, b = blockIdx.z;
   const int64_t pair = (int64_t)b * a.c.Hkv + g;
   const int n = a.moves[pair];
   const int32_t* give = a.lists + pair * 2 * a.max_move;
-  const int i0 = (int)blockIdx.x * kMvRows;
-  if (i0 < n) move_rows(a.c, b, g, give, give + a.max_move, i0, min(n, i0 + kMvRows), threadIdx.x, kMvThreads);
+  const int i0 = ((int)blockIdx.x * (kMvThreads / 32) + (threadIdx.x >> 5)) * kRowItems;
+  if (i0 < n) move_rows<D>(a.c, b, g, give, give + a.max_move, i0, n);
 }
 
 int64_t evict_max_move(int64_t max_len, int64_t budget) {
@@ -622,9 +639,9 @@ extern "C" kvc_status kvc_paged_evict(const kvc_paged_cache* c, int64_t max_len,
   const cudaStream_t st = (cudaStream_t)stream;
   s = max_len <= kEvSmall ? launch_evict<256>(a, st) : launch_evict<1024>(a, st);
   if (s != KVC_OK || a.in_place) return s;
-  const Launch l(dim3((unsigned)((a.max_move + kMvRows - 1) / kMvRows), (unsigned)a.c.Hkv, (unsigned)a.c.batch),
+  const Launch l(dim3((unsigned)((a.max_move + kMvSpan - 1) / kMvSpan), (unsigned)a.c.Hkv, (unsigned)a.c.batch),
                  dim3(kMvThreads), 0, st);
-  KVC_CUDA_TRY(l.run(evict_move_kernel, a));
+  KVC_CUDA_TRY(a.c.d == 128 ? l.run(evict_move_kernel<128>, a) : l.run(evict_move_kernel<64>, a));
   count_launch();
   return KVC_OK;
 }
