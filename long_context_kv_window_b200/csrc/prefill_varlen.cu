@@ -33,6 +33,17 @@
 // threads per row halve the time the softmax takes, and the output MMA of a
 // half starts when that half's P is there.
 //
+// Measured (32/8 heads, d = 128): 32K tokens 6.9 ms in bursts (1.27 PFLOP/s, 75 %
+// of the measured burst rate of a library GEMM), 7.9 to 8.1 ms for seconds on end
+// (1.1 PFLOP/s, 79 % of the sustained rate; the board's power bounds it: SM clock
+// 1.55 GHz).  A key tile takes 3400 cycles of 2048 that its MMAs need: per MMA
+// tile the softmax 1700 (1450 of them the exponentials, 1024 at the MUFU's rate)
+// and MMAs with their hand-overs 1700.  Tried: a part of the exponentials on the
+// FMA pipe as polynomials (1/8: 3 %, 1/2: 10 % slower: more instructions, more
+// power); 64-key logits in four chains (19 % slower: N = 64 MMAs take 450 cycles
+// where N = 128 ones take 512); half-signals of P; polling instead of suspended
+// waits (2 to 4 % slower).
+//
 // Keys a row does not see are masked before the max.  A masked value row still
 // meets p = 0 in the MMA, and 0 * inf = NaN; so the value tiles in which some
 // row of the block masks a key are looked over first, infinities and NaN in
