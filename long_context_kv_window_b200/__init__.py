@@ -746,10 +746,14 @@ class PagedCache:
                    pos=torch.zeros(shape, dtype=i32, device=device),
                    next_pos=torch.zeros(batch, dtype=i32, device=device))
 
-    def _workspace(self, call: str, size_args: tuple, handle: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-        """A workspace of `call` on the stream of that handle.  Its counters,
-        which start at zero and come first, depend on the cache alone, so a
-        workspace serves every call that needs no more bytes."""
+    def _workspace(self, ws: Optional[torch.Tensor], call: str, size_args: tuple, handle: int,
+                   stream: Optional[torch.cuda.Stream]) -> Tuple[int, int]:
+        """Address and bytes of the caller's workspace, or of the one kept for
+        `call` on the stream of that handle.  Its counters, which start at zero
+        and come first, depend on the cache alone, so a workspace serves every
+        call that needs no more bytes."""
+        if ws is not None:
+            return ws.data_ptr(), _ws_bytes(ws, self.device)
         need = self._need.get((call, size_args))
         if need is None:
             out = ctypes.c_size_t(0)
@@ -757,14 +761,16 @@ class PagedCache:
                          ctypes.byref(out)), call + "_workspace_size")
             need = self._need[call, size_args] = max(int(out.value), 1)
         capturing = torch.cuda.is_current_stream_capturing()
-        ws = None if capturing else self._ws.get((call, handle))
-        if ws is None or ws.numel() < need:
-            with torch.cuda.stream(stream):  # None: the current stream
-                ws = _workspace(need, self.device)
-                ws[:4 * self.batch * self.num_kv_heads].zero_()
-            if not capturing:
-                self._ws[call, handle] = ws
-        return ws
+        if not capturing:
+            kept = self._ws.get((call, handle))
+            if kept is not None and kept[2] >= need:
+                return kept[1:]
+        with torch.cuda.stream(stream):  # None: the current stream
+            ws = _workspace(need, self.device)
+            ws[:4 * self.batch * self.num_kv_heads].zero_()
+        if not capturing:
+            self._ws[call, handle] = ws, ws.data_ptr(), need
+        return ws.data_ptr(), need
 
     def _max_len(self, max_len: Optional[int]) -> int:
         return self.capacity if max_len is None else int(max_len)
@@ -782,10 +788,9 @@ def kvc_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seq
     dev = cache.device
     if v is None:
         raise ValueError("v is missing")
-    _kv_pair(k, v)
-    total, Hkv, d = k.shape
-    if k.device != dev:
+    if _kv_pair(k, v) != dev:
         raise ValueError(f"k is on {k.device}, the cache on {dev}")
+    total, Hkv, d = k.shape
     if Hkv != cache.num_kv_heads or d != cache.head_dim:
         raise ValueError(f"k and v must be [total][{cache.num_kv_heads}][{cache.head_dim}], got {tuple(k.shape)}")
     if cu_seqlens is None:
@@ -806,10 +811,10 @@ def kvc_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seq
         _dense(scores, "scores", (Hkv, total), torch.float32, dev)
     _err_word(dev_err, dev)
     st = _raw_stream(stream, dev)
-    if ws is None:
-        ws = cache._workspace("kvc_paged_append", (), st, stream)
-    _check(_call(dev, lib().kvc_paged_append, cache._ref, _adr(k), _adr(v), _stride(k, 0), _stride(k, 1),
-                 _adr(cu_seqlens), total, int(max_seqlen), _adr(idx), kk, _adr(scores), _adr(ws), _ws_bytes(ws, dev),
+    at, nbytes = cache._workspace(ws, "kvc_paged_append", (), st, stream)
+    sn, sh, _ = k.stride()
+    _check(_call(dev, lib().kvc_paged_append, cache._ref, k.data_ptr(), v.data_ptr(), sn if total > 1 else Hkv * d,
+                 sh if Hkv > 1 else d, _adr(cu_seqlens), total, int(max_seqlen), _adr(idx), kk, _adr(scores), at, nbytes,
                  _adr(dev_err), st), "kvc_paged_append")
     return cache
 
@@ -841,11 +846,10 @@ def kvc_paged_decode_attention(q: torch.Tensor, cache: PagedCache, scale: Option
     _err_word(dev_err, dev)
     max_len = cache._max_len(max_len)
     st = _raw_stream(stream, dev)
-    if ws is None:
-        ws = cache._workspace("kvc_paged_decode", (H, max_len, int(accumulate)), st, stream)
+    at, nbytes = cache._workspace(ws, "kvc_paged_decode", (H, max_len, int(accumulate)), st, stream)
     sc = float(1.0 / math.sqrt(d) if scale is None else scale)
-    _check(_call(dev, lib().kvc_paged_decode_attention, cache._ref, _adr(q), _stride(q, 0), _stride(q, 1), H, sc, max_len,
-                 int(accumulate), _adr(out), _adr(lse), _adr(ws), _ws_bytes(ws, dev), _adr(dev_err), st),
+    _check(_call(dev, lib().kvc_paged_decode_attention, cache._ref, q.data_ptr(), _stride(q, 0), _stride(q, 1), H, sc,
+                 max_len, int(accumulate), out.data_ptr(), lse.data_ptr(), at, nbytes, _adr(dev_err), st),
            "kvc_paged_decode_attention")
     _used_on(stream, made_out, made_lse)
     return out, lse
@@ -865,10 +869,9 @@ def kvc_paged_evict(cache: PagedCache, budget: int, recent: int, max_len: Option
     _err_word(dev_err, dev)
     max_len = cache._max_len(max_len)
     st = _raw_stream(stream, dev)
-    if ws is None:
-        ws = cache._workspace("kvc_paged_evict", (max_len, int(budget)), st, stream)
-    _check(_call(dev, lib().kvc_paged_evict, cache._ref, max_len, int(budget), int(recent), _adr(ws),
-                 _ws_bytes(ws, dev), _adr(dev_err), st), "kvc_paged_evict")
+    at, nbytes = cache._workspace(ws, "kvc_paged_evict", (max_len, int(budget)), st, stream)
+    _check(_call(dev, lib().kvc_paged_evict, cache._ref, max_len, int(budget), int(recent), at, nbytes, _adr(dev_err),
+                 st), "kvc_paged_evict")
     return cache
 
 

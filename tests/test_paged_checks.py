@@ -124,7 +124,8 @@ def test_prefill_varlen_refusals(clib):
 @pytest.fixture
 def lib(fake_lib, monkeypatch):  # noqa: F811
     monkeypatch.setattr(kvc, "_raw_stream", lambda stream, dev: 0)
-    monkeypatch.setattr(kvc.PagedCache, "_workspace", lambda self, *a: torch.empty(16, dtype=torch.uint8))
+    monkeypatch.setattr(kvc.PagedCache, "_workspace",
+                        lambda self, ws, *a: (0, 16 if ws is None else kvc._ws_bytes(ws, self.device)))
     monkeypatch.setattr(kvc, "_used_on", lambda stream, *made: None)
     return fake_lib
 
