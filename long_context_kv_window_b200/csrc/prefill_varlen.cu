@@ -25,13 +25,12 @@
 // follow the max: later tiles take no max.  Where a row's sum over 64 keys
 // passes 2^60 -- logits 41 above all of the first 128 keys -- the block is
 // computed again: a pass over the logits finds the rows' maxima, and the pass
-// after it uses those.
+// after it uses those.  (So it is where a row's first 128 logits are all -inf.)
 //
 // P overwrites the logits it came from (the TMEM has no room for a second
 // buffer), so logits, softmax and output of an MMA tile follow one another, and
 // while one tile is at the tensor core the other is at its softmax.  Two
-// threads per row halve the time the softmax takes, and the output MMA of a
-// half starts when that half's P is there.
+// threads per row halve the time the softmax takes.
 //
 // Measured (32/8 heads, d = 128): 32K tokens 6.9 ms in bursts (1.27 PFLOP/s, 75 %
 // of the measured burst rate of a library GEMM), 7.9 to 8.1 ms for seconds on end
@@ -502,7 +501,10 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         if (pass == 1) {
           m_ref = fmaxf(m_ref, row_max());
         } else {
-          if (pass == 0 && t == 0) m_ref = both(row_max(), larger);  // the first tile sets the references
+          if (pass == 0 && t == 0) {  // the first tile sets the references, if it has a logit above -inf
+            m_ref = both(row_max(), larger);
+            past = m_ref == -INFINITY && limit >= kf + kVT;
+          }
           // a row that has seen no key yet has only x = -inf: p = 2^-inf = 0
           const float ref = m_ref == -INFINITY ? 0.f : m_ref;
           const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);

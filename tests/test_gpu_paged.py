@@ -155,6 +155,28 @@ def test_prefill_varlen_logits_far_above_the_first_tile(n, at, G):
     _close(_np(out), w_out, tol, "out")
 
 
+def test_prefill_varlen_first_keys_at_minus_infinity():
+    """The first 128 logits of every row are -inf, the others far below 0: the
+    later rows are those of a sequence without the first keys."""
+    rng = np.random.default_rng(5)
+    n, H, d = 400, 2, 128
+    q, _ = _bf16(rng, n, H, d)
+    q[:, :, :2] = 2.0
+    k, _ = _bf16(rng, n, 1, d)
+    k[:, :, :2] = 0.0
+    k[128:, :, 1] = -2000.0  # logits near -4000 / sqrt(128)
+    v, vd = _bf16(rng, n, 1, d)
+    qd = torch.from_numpy(q).to(torch.bfloat16).cuda()
+    k[:128, :, 0] = -np.inf
+    kd = torch.from_numpy(k).to(torch.bfloat16).cuda()
+    k = _np(kd)
+    out, lse = _run_prefill(qd, kd, vd, [n], [n])
+    w_out, w_lse, tol, tol_lse = ref.prefill_varlen(q[128:], k[128:], v[128:], [0, n - 128], [0, n - 128], 1 / math.sqrt(d))
+    assert w_lse.max() < -300
+    _close(_np(lse)[128:], w_lse, tol_lse, "lse")
+    _close(_np(out)[128:], w_out, tol, "out")
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_prefill_varlen_fused_projection_views_and_rows_behind(d):
     """q, k, v as views of one [n][(H + 2 Hkv) d] projection; rows behind the
@@ -209,6 +231,21 @@ def test_prefill_varlen_masked_places_may_hold_anything(what, bad):
         assert torch.equal(lse, clean_lse)
     elif math.isnan(bad):
         assert torch.isnan(hit).all()
+
+
+def test_prefill_varlen_head_major_layout():
+    """q, k, v stored [heads][n][d], seen as [n][heads][d]."""
+    rng = np.random.default_rng(27)
+    lens, H, Hkv, d = [150, 60], 6, 2, 64
+    n = sum(lens)
+    q, qd = _bf16(rng, H, n, d)
+    k, kd = _bf16(rng, Hkv, n, d)
+    v, vd = _bf16(rng, Hkv, n, d)
+    out, lse = _run_prefill(*(x.transpose(0, 1) for x in (qd, kd, vd)), lens, lens)
+    q, k, v = (x.transpose(1, 0, 2) for x in (q, k, v))
+    w_out, w_lse, tol, tol_lse = ref.prefill_varlen(q, k, v, _cu(lens), _cu(lens), 1 / math.sqrt(d))
+    _close(_np(lse), w_lse, tol_lse, "lse")
+    _close(_np(out), w_out, tol, "out")
 
 
 def test_prefill_varlen_agrees_with_the_single_sequence_call():
