@@ -18,13 +18,13 @@ namespace {
 
 // ------------------------------------------------------------------- append
 // A copy: per kept entry and KV head d bf16 values of k and of v in, the same
-// out, and (weight, position).  A warp takes kRowItems (entry, head)
-// items: one lane each finds its token, half the lanes (or a quarter, d = 64)
-// request an item's k row and as many its v row, all items before the first
-// store, and the lanes of the items find the places meanwhile.  Items go head by head within an entry
-// where the tokens lie so (a whole prompt), entry by entry within a head where
-// a list selects them (the list and the pages then run on).  Lengths move on
-// once every CTA has read them: the last CTA of the grid (a ticket counter,
+// out, and (weight, position).  A warp takes kRowItems (entry, head) items: one
+// lane each finds its token, half the lanes (or a quarter, d = 64) request an
+// item's k row and as many its v row, all items before the first store, and
+// the lanes of the items find the places meanwhile.  Items go head by head
+// within an entry where the tokens lie so (a whole prompt), entry by entry
+// within a head where a list selects them (the list and the pages then run
+// on).  Lengths move on once every CTA has read them: the last CTA of the grid (a ticket counter,
 // returned to zero) adds the new entries.  8 x 8 x 1024 selected rows (67 MB
 // in all) take 19.6 us cold, 3.4 TB/s: scattered reads of 256 bytes bound it.
 // One token for each of 64 sequences is four dependent round trips, 5 us.
@@ -147,11 +147,12 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const AppArgs a) {
 // A pair (KV head, sequence) is a CTA, or a cluster of up to 8 where the pairs
 // are few and long, each with a run of the slots.  Keys are the
 // order-preserving uint32 image of the weights (recent entries the largest key,
-// NaN 0), kept in shared memory where they fit.  One entry too many -- every decoding step -- needs the lowest
-// ranked entry only, one reduction.  Otherwise the budget-th largest key T is
-// found by histograms of 2048 equal bins over the range of the keys, then over
-// the bin that holds it, until the bin is one key or is kept whole (weights
-// span few exponents, so bins over their range part them better than fixed
+// NaN 0), kept in shared memory where they fit.  One entry too many -- every
+// decoding step -- needs the lowest ranked entry only, one reduction.
+// Otherwise the budget-th largest key T is found by histograms of 2048 equal
+// bins over the range of the keys, then over the bin that holds it, until the
+// bin is one key or is kept whole (weights span few exponents, so bins over
+// their range part them better than fixed
 // digits do).  Warps then own runs of slots: counted with ballots, prefixed
 // once over the warps, listed with ballots: the slots given up below the
 // budget and the kept slots above it, both ascending.

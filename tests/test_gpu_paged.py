@@ -523,6 +523,39 @@ def test_paged_decode_is_deterministic():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+def test_pages_past_the_reach_of_32_bits():
+    """A pool of more than 2^32 elements: its last pages are written, read and moved within."""
+    rng = np.random.default_rng(25)
+    P, Hkv, page, d = 16450, 8, 128, 128
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("not enough device memory")
+    both = torch.empty((P, 2, Hkv, page, d), dtype=torch.bfloat16, device="cuda")
+    assert (P - 3) * both.stride(0) > 2 ** 32
+    small = Paged(rng, [0, 0], Hkv, d, page, room=250)  # the same entries in a small pool
+    table = _dev_i32([[P - 1, P - 3], [P - 2, 0]])
+    shape = (P, Hkv, page)
+    big = kvc.PagedCache(both[:, 0], both[:, 1], table, _dev_i32([0, 0]),
+                         weights=torch.zeros(shape, device="cuda"), pos=torch.zeros(shape, dtype=torch.int32, device="cuda"),
+                         next_pos=_dev_i32([3, 3]))
+    lens = [240, 100]
+    _, k = _bf16(rng, sum(lens), Hkv, d)
+    _, v = _bf16(rng, sum(lens), Hkv, d)
+    sc = torch.rand((Hkv, sum(lens)), device="cuda")
+    _, q = _bf16(rng, 2, 2 * Hkv, d)
+    got = []
+    for c in (small.cache, big):
+        kvc.kvc_paged_append(c, k, v, _dev_i32(_cu(lens)), 240, scores=sc, dev_err=small.err)
+        a = kvc.kvc_paged_decode_attention(q, c, max_len=256, accumulate=True, dev_err=small.err)
+        kvc.kvc_paged_evict(c, 90, 10, max_len=256, dev_err=small.err)
+        b = kvc.kvc_paged_decode_attention(q, c, max_len=256, dev_err=small.err)
+        at = c.block_table[0, 0].long()
+        got.append([*a, *b, c.k[at, :, :90], c.v[at, :, :90], c.weights[at, :, :90], c.pos[at, :, :90]])
+    torch.cuda.synchronize()
+    assert small.err.item() == 0
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
 def test_paged_decode_flags_bad_pages_and_lengths():
     rng = np.random.default_rng(21)
     for kind in ("page", "long", "negative"):
