@@ -544,6 +544,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       const bool seen = limit >= kf && nt > 0;  // no key of this CTA otherwise
       const float inv = seen ? 1.f / sum_row : 0.f;
       const bool dirty = *(volatile int*)&bars->dirty != 0;
+      uint8_t* stage = sm + L::kRing + (warp - 4) * 32 * 80;  // this warp's rows
 #pragma unroll 1
       for (int c0 = 0; c0 < D / 2; c0 += 32) {
         uint32_t o[32];
@@ -551,12 +552,12 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
           KVC_TMEM_WAIT_LD32(o);
         }
-        if (!mine || (!a.out && !a.part_o)) continue;
+        if (!a.out && !a.part_o) continue;
         float f[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) f[e] = seen ? __uint_as_float(o[e]) * inv : 0.f;
         const int col = (D / 2) * hf + c0;
-        if (dirty)  // non-finite values of the checked tiles, where this row sees them
+        if (dirty && mine)  // non-finite values of the checked tiles, where this row sees them
           for (int j = kf + t_mask * kVT; j <= limit && j < kf + nt * kVT; ++j) {
             const uint16_t* vr = a.v + (int64_t)(k0 + j) * a.v_sn + (int64_t)g * a.v_sh + col;
 #pragma unroll
@@ -567,11 +568,13 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           }
         if (a.part_o) {
           float4* po = reinterpret_cast<float4*>(a.part_o + (((int64_t)split * a.total_q + row) * a.H + h) * D + col);
+          if (mine)
 #pragma unroll
-          for (int u = 0; u < 8; ++u) po[u] = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
+            for (int u = 0; u < 8; ++u) po[u] = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
           continue;
         }
-        uint4* dst = reinterpret_cast<uint4*>(a.out + (row * a.H + h) * D + col);
+        // through the ring (free now, 80-byte rows), so that a store covers 64
+        // bytes of 8 rows instead of 16 bytes of 32
 #pragma unroll
         for (int v8 = 0; v8 < 4; ++v8) {
           uint32_t w[4];
@@ -580,8 +583,17 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             const __nv_bfloat162 hp = __floats2bfloat162_rn(f[8 * v8 + 2 * u], f[8 * v8 + 2 * u + 1]);
             w[u] = *reinterpret_cast<const uint32_t*>(&hp);
           }
-          dst[v8] = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(stage + lane * 80 + v8 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int k8 = 0; k8 < 4; ++k8) {
+          const int src = 8 * k8 + (lane >> 2);
+          const int64_t at = __shfl_sync(0xffffffffu, mine ? (row * a.H + h) * D : -1, src);
+          const uint4 y = *reinterpret_cast<const uint4*>(stage + src * 80 + (lane & 3) * 16);
+          if (at >= 0) *reinterpret_cast<uint4*>(a.out + at + col + (lane & 3) * 8) = y;
+        }
+        __syncwarp();
       }
       if (mine && hf == 0) {
         const double z = (double)m_ref + log2((double)sum_row);
