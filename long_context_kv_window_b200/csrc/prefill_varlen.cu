@@ -25,10 +25,12 @@
 // follow the max: later tiles take no max.  Where a row's sum over 64 keys
 // passes 2^60 -- logits 41 above all of the first 128 keys -- the block is
 // computed again: a pass over the logits finds the rows' maxima, and the pass
-// after it uses those.  (So it is where a row's first 128 logits are all -inf.)
+// after it uses those for the rows that need them.  (So it is where a row's
+// first 128 logits are all -inf.)
 //
-// P overwrites the logits it came from (the TMEM has no room for a second
-// buffer), so logits, softmax and output of an MMA tile follow one another, and
+// P overwrites the logits it came from (the TMEM has room for a second buffer
+// only with 80-key tiles, where the narrower MMAs cost more than the overlap
+// gives: 32K tokens 8.4 ms against 7.9), so logits, softmax and output of an MMA tile follow one another, and
 // while one tile is at the tensor core the other is at its softmax.  Two
 // threads per row halve the time the softmax takes.
 //
@@ -286,7 +288,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   }
   int issued = 0, last_pass = 0;  // producer: K and V tiles requested
   // Pass 0 computes; if a row passed its reference by too much, pass 1 finds
-  // every row's max and pass 2 computes with that.  The ring and the barriers
+  // every row's max and pass 2 computes with that of the rows that did.  The ring and the barriers
   // go on counting from pass to pass.
   auto again = [&](int pass) {
     tc::named_bar_sync(15, kVBlock);
@@ -460,7 +462,8 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       return hf ? *swap : mine_x;
     };
     auto larger = [](float x0, float x1) { return fmaxf(x0, x1); };
-    float m_ref = -INFINITY;
+    float m_ref = -INFINITY, top = -INFINITY;
+    bool past = false;  // the row needs its maximum as reference
     double l = 0.0;  // this thread's half of the row sum
     bool ok = true;
     uint32_t x[64];
@@ -475,9 +478,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     const bool releases = wq == 0 && hf == 0 && lane == 0;  // tells the producer for this tile
     for (int pass = 0; pass == 0 || again(pass - 1); ++pass) {
       const int ub = pass * nt, base = ring_base(pass);
-      bool past = false;
       l = 0.0;
-      if (pass == 1) m_ref = -INFINITY;
       for (int t = 0; t < nt; ++t) {
         if (!tc::mbar_wait(&bars->s_full[i], (ub + t) & 1, abort_flag)) ok = false;
         if (releases && ok) {  // S(t) is there: K(t) and, before it, V(t - 1) are read
@@ -499,7 +500,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             if (e > lim) x[e] = __float_as_uint(-INFINITY);
         }
         if (pass == 1) {
-          m_ref = fmaxf(m_ref, row_max());
+          top = fmaxf(top, row_max());
         } else {
           if (pass == 0 && t == 0) {  // the first tile sets the references, if it has a logit above -inf
             m_ref = both(row_max(), larger);
@@ -529,7 +530,9 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         if (lane == 0 && ok) tc::mbar_arrive(&bars->p_full[i]);
       }
       if (pass == 1) {
-        m_ref = both(m_ref, larger);
+        // the other rows keep theirs, and their results to the last bit
+        top = both(top, larger);
+        if (both(past ? 1.f : 0.f, larger) > 0.f) m_ref = top;
       } else {
         if (nt > 0 && !tc::mbar_wait(&bars->o_done[i], pass >> 1, abort_flag)) ok = false;
         if (nt > 0 && releases && ok) tc::mbar_arrive(&bars->empty[(base + 2 * nt - 1) % L::kStages]);

@@ -233,6 +233,22 @@ def test_prefill_varlen_masked_places_may_hold_anything(what, bad):
         assert torch.isnan(hit).all()
 
 
+def test_prefill_varlen_rows_beside_one_that_outgrows_its_reference():
+    """Keys past the first tile that lift the rows behind them by far, to +inf
+    among them, leave the rows before them as they were, bit for bit."""
+    rng = np.random.default_rng(31)
+    lens, H, d = [300], 4, 128
+    q, qd = _bf16(rng, 300, H, d)
+    k, kd = _bf16(rng, 300, 1, d)
+    v, vd = _bf16(rng, 300, 1, d)
+    clean, clean_lse = _run_prefill(qd, kd, vd, lens, lens)
+    for bad in (float("inf"), 300.0):
+        kd[270, 0] = bad
+        out, lse = _run_prefill(qd, kd, vd, lens, lens)
+        assert torch.equal(out[:270], clean[:270]) and torch.equal(lse[:270], clean_lse[:270])
+        assert not torch.equal(out[270:], clean[270:])
+
+
 def test_prefill_varlen_head_major_layout():
     """q, k, v stored [heads][n][d], seen as [n][heads][d]."""
     rng = np.random.default_rng(27)
