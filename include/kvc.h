@@ -395,7 +395,9 @@ kvc_status kvc_prefill_varlen_workspace_size(int32_t num_heads, int32_t num_kv_h
  * fp32 accumulation; the probabilities enter the output contraction as bf16
  * and the output is normalised by the sum of the fp32 ones, which is the
  * log-sum-exp's too: |error| <= 2^-8 (mean of |v| under the probabilities) for
- * the former rounding and as much for the output's.  Deterministic.
+ * the former rounding and as much for the output's.  The probabilities are
+ * taken relative to a row's first keys, up to 2^60 each: finite values above
+ * 2^42 in v may overflow the sums.  Deterministic.
  */
 kvc_status kvc_prefill_attention_varlen(const uint16_t* q, int64_t q_stride_n, int64_t q_stride_h, const uint16_t* k,
                                         int64_t k_stride_n, int64_t k_stride_h, const uint16_t* v, int64_t v_stride_n,
@@ -432,7 +434,7 @@ typedef struct kvc_paged_cache {
   int64_t table_stride;       /* >= max_pages */
   int32_t num_pages;          /* pages in the pool */
   int32_t page_size;          /* entries per page: 16, 32, 64, 128 or 256 */
-  int32_t max_pages;          /* pages per sequence the table has room for */
+  int32_t max_pages;          /* pages per sequence the table has room for: at most 2^30 entries */
   int32_t batch;              /* 1..1024 */
   int32_t num_kv_heads;
   int32_t head_dim;           /* 64 or 128 */
@@ -495,7 +497,8 @@ kvc_status kvc_paged_decode_workspace_size(const kvc_paged_cache* c, int32_t num
  * entries is not used, whatever it is (infinities and NaN included).
  *  q        [B][H][d] bf16, element (b, h, c) at q[b*q_stride_b + h*q_stride_h + c];
  *           16-byte aligned, strides multiples of 8
- *  max_len  upper bound of seq_lens (host value), <= max_pages * page_size
+ *  max_len  upper bound of seq_lens (host value), <= max_pages * page_size;
+ *           batch * max_len below 2^36, batch * num_kv_heads * max_len below 2^40
  *  out      [B][H][d] fp32, contiguous, 16-byte aligned
  *  lse      [B][H] fp32 contiguous, or NULL
  *  ws       kvc_paged_decode_workspace_size(...) bytes, 256-B aligned,
@@ -508,7 +511,8 @@ kvc_status kvc_paged_decode_workspace_size(const kvc_paged_cache* c, int32_t num
  * At most 16 query heads per KV head.  Pages may be shared by sequences
  * unless `accumulate` is set (which also wants the weights 16-byte aligned).
  * fp32 accumulation from the bf16 values and the
- * fp32 probabilities (as three bf16 terms).  Deterministic.
+ * fp32 probabilities (as three bf16 terms, relative to a maximum within 2^8:
+ * finite values above 2^80 in v may overflow the sums).  Deterministic.
  */
 kvc_status kvc_paged_decode_attention(const kvc_paged_cache* c, const uint16_t* q, int64_t q_stride_b,
                                       int64_t q_stride_h, int32_t num_heads, float scale, int64_t max_len,

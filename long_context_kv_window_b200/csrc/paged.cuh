@@ -43,7 +43,7 @@ inline kvc_status check_paged(const kvc_paged_cache* c, Paged* out) {
   KVC_CHECK_ARG(c->batch >= 1 && c->batch <= 1024, "batch must be in 1..1024");
   KVC_CHECK_ARG(c->num_kv_heads >= 1 && c->num_kv_heads <= 65535, "num_kv_heads must be in 1..65535");
   KVC_CHECK_ARG(c->num_pages >= 1 && c->max_pages >= 1, "num_pages and max_pages must be positive");
-  KVC_CHECK_ARG((int64_t)c->max_pages * page < (int64_t(1) << 31), "max_pages * page_size must be below 2^31");
+  KVC_CHECK_ARG((int64_t)c->max_pages * page <= (int64_t(1) << 30), "max_pages * page_size must be at most 2^30");
   KVC_CHECK_ARG(c->table_stride >= c->max_pages, "table_stride must be >= max_pages");
   KVC_CHECK_ARG(c->page_stride >= (int64_t)c->num_kv_heads * page * c->head_dim && c->page_stride % 8 == 0,
                 "page_stride must cover a page and be a multiple of 8 elements");

@@ -721,6 +721,10 @@ kvc_status check_paged_decode(const Paged& c, int32_t H, int64_t max_len) {
   KVC_CHECK_ARG(H >= 1 && H % c.Hkv == 0, "num_heads must be a positive multiple of num_kv_heads");
   if (H / c.Hkv > kPdMaxG) return fail(KVC_ERR_UNSUPPORTED, "at most 16 query heads per KV head");
   KVC_CHECK_ARG(max_len >= 1 && max_len <= c.room(), "need 1 <= max_len <= max_pages * page_size");
+  // the kernels count the places of all sequences, and the spans of all pairs, in 32 bits
+  KVC_CHECK_ARG((int64_t)c.batch * ((max_len + kPdTile - 1) / kPdTile + kPdPairCost) < (int64_t(1) << 31) &&
+                    (int64_t)c.batch * c.Hkv * ((max_len + kWtSpan - 1) / kWtSpan) < (int64_t(1) << 31),
+                "batch * max_len must be below 2^36, and batch * num_kv_heads * max_len below 2^40");
   return KVC_OK;
 }
 

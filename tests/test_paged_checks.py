@@ -212,3 +212,19 @@ def test_prefill_varlen_binding(lib, monkeypatch):
                   ((q[:, :, ::2], k[:, :, ::2], k[:, :, ::2], cu, cu, 5, 6), {})):
         with pytest.raises((ValueError, TypeError)):
             kvc.kvc_prefill_attention_varlen(*a, **kw)
+
+
+def test_paged_sizes_beyond_the_kernels_counters(clib):
+    n = ctypes.byref(ctypes.c_size_t())
+    big = _cache(batch=1024, page_size=256, max_pages=1 << 22, table_stride=1 << 22,  # room for 2^30 entries each
+                 page_stride=1 << 15)
+    c = ctypes.byref(big)
+    assert clib.kvc_paged_decode_workspace_size(c, 2, (1 << 26) - 1024, 0, n) == 0
+    assert clib.kvc_paged_decode_workspace_size(c, 2, (1 << 27), 0, n) == 1  # 2^37 entries
+    assert clib.kvc_paged_decode_attention(c, PTR, 128, 64, 2, 0.125, 1 << 27, 0, PTR, None, PTR, 1 << 40, None,
+                                           None) == 1
+    wide = _cache(batch=1024, page_size=256, max_pages=1 << 22, table_stride=1 << 22, num_kv_heads=1 << 15,
+                  page_stride=256 << 21)
+    assert clib.kvc_paged_decode_workspace_size(ctypes.byref(wide), 1 << 15, 1 << 16, 0, n) == 1  # 2^41 of all heads
+    over = ctypes.byref(_cache(page_size=256, max_pages=(1 << 22) + 1, table_stride=1 << 23, page_stride=1 << 15))
+    assert clib.kvc_paged_append_workspace_size(over, n) == 1 and "2^30" in kvc.last_error()
