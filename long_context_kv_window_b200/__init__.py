@@ -760,7 +760,11 @@ class PagedCache:
             _check(_call(self.device, getattr(lib(), call + "_workspace_size"), self._ref, *size_args,
                          ctypes.byref(out)), call + "_workspace_size")
             need = self._need[call, size_args] = max(int(out.value), 1)
-        capturing = torch.cuda.is_current_stream_capturing()
+        if stream is None and torch.cuda.current_device() == self.device.index:
+            capturing = torch.cuda.is_current_stream_capturing()
+        else:  # the state of the stream the call runs on
+            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
         if not capturing:
             kept = self._ws.get((call, handle))
             if kept is not None and kept[2] >= need:

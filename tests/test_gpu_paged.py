@@ -828,6 +828,29 @@ def test_two_streams_and_two_graphs_share_no_workspace():
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
+def test_a_captured_call_names_its_stream():
+    """The stream a call is given is being captured, the current one is not: the
+    workspace made then is the graph's, not one kept for later calls, which
+    would find its counters unset until the graph's first replay."""
+    rng = np.random.default_rng(73)
+    t = Paged(rng, [900, 5, 333], 2, 64, 16)
+    q = _bf16(rng, 3, 4, 64)[1]
+    out, lse = torch.empty((3, 4, 64), device="cuda"), torch.empty((3, 4), device="cuda")
+    want = kvc.kvc_paged_decode_attention(q, t.cache)[0]
+    torch.cuda.synchronize()
+    s, side, g = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        with torch.cuda.stream(side):
+            kvc.kvc_paged_decode_attention(q, t.cache, out=out, lse=lse, stream=s)
+    assert not any(handle == s.cuda_stream for _, handle in t.cache._ws)
+    got = kvc.kvc_paged_decode_attention(q, t.cache, stream=s)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 # --------------------------------------------------------------------------- #
 # bounded waits
 # --------------------------------------------------------------------------- #
