@@ -15,6 +15,7 @@ import ctypes
 import functools
 import math
 import os
+import threading
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
@@ -731,6 +732,7 @@ class PagedCache:
         self._c = PagedCacheStruct(*adr, strides[0], _stride(block_table, 0), num_pages, page, self.max_pages, B, Hkv, d)
         self._ref = ctypes.byref(self._c)
         self._ws, self._need = {}, {}
+        self._lock = threading.Lock()  # a call's kernels follow one another: they share a kept workspace
 
     @classmethod
     def allocate(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, batch: int, max_pages: int,
@@ -815,11 +817,12 @@ def kvc_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seq
         _dense(scores, "scores", (Hkv, total), torch.float32, dev)
     _err_word(dev_err, dev)
     st = _raw_stream(stream, dev)
-    at, nbytes = cache._workspace(ws, "kvc_paged_append", (), st, stream)
     sn, sh, _ = k.stride()
-    _check(_call(dev, lib().kvc_paged_append, cache._ref, k.data_ptr(), v.data_ptr(), sn if total > 1 else Hkv * d,
-                 sh if Hkv > 1 else d, _adr(cu_seqlens), total, int(max_seqlen), _adr(idx), kk, _adr(scores), at, nbytes,
-                 _adr(dev_err), st), "kvc_paged_append")
+    with cache._lock:
+        at, nbytes = cache._workspace(ws, "kvc_paged_append", (), st, stream)
+        _check(_call(dev, lib().kvc_paged_append, cache._ref, k.data_ptr(), v.data_ptr(), sn if total > 1 else Hkv * d,
+                     sh if Hkv > 1 else d, _adr(cu_seqlens), total, int(max_seqlen), _adr(idx), kk, _adr(scores), at,
+                     nbytes, _adr(dev_err), st), "kvc_paged_append")
     return cache
 
 
@@ -850,11 +853,12 @@ def kvc_paged_decode_attention(q: torch.Tensor, cache: PagedCache, scale: Option
     _err_word(dev_err, dev)
     max_len = cache._max_len(max_len)
     st = _raw_stream(stream, dev)
-    at, nbytes = cache._workspace(ws, "kvc_paged_decode", (H, max_len, int(accumulate)), st, stream)
     sc = float(1.0 / math.sqrt(d) if scale is None else scale)
-    _check(_call(dev, lib().kvc_paged_decode_attention, cache._ref, q.data_ptr(), _stride(q, 0), _stride(q, 1), H, sc,
-                 max_len, int(accumulate), out.data_ptr(), lse.data_ptr(), at, nbytes, _adr(dev_err), st),
-           "kvc_paged_decode_attention")
+    with cache._lock:
+        at, nbytes = cache._workspace(ws, "kvc_paged_decode", (H, max_len, int(accumulate)), st, stream)
+        _check(_call(dev, lib().kvc_paged_decode_attention, cache._ref, q.data_ptr(), _stride(q, 0), _stride(q, 1), H,
+                     sc, max_len, int(accumulate), out.data_ptr(), lse.data_ptr(), at, nbytes, _adr(dev_err), st),
+               "kvc_paged_decode_attention")
     _used_on(stream, made_out, made_lse)
     return out, lse
 
@@ -873,9 +877,10 @@ def kvc_paged_evict(cache: PagedCache, budget: int, recent: int, max_len: Option
     _err_word(dev_err, dev)
     max_len = cache._max_len(max_len)
     st = _raw_stream(stream, dev)
-    at, nbytes = cache._workspace(ws, "kvc_paged_evict", (max_len, int(budget)), st, stream)
-    _check(_call(dev, lib().kvc_paged_evict, cache._ref, max_len, int(budget), int(recent), at, nbytes, _adr(dev_err),
-                 st), "kvc_paged_evict")
+    with cache._lock:
+        at, nbytes = cache._workspace(ws, "kvc_paged_evict", (max_len, int(budget)), st, stream)
+        _check(_call(dev, lib().kvc_paged_evict, cache._ref, max_len, int(budget), int(recent), at, nbytes,
+                     _adr(dev_err), st), "kvc_paged_evict")
     return cache
 
 

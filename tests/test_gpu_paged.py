@@ -851,6 +851,34 @@ def test_a_captured_call_names_its_stream():
     assert torch.equal(out, want)
 
 
+def test_threads_accumulate_on_one_stream():
+    """Accumulating calls of several host threads on one stream: each adds its
+    own query's attention."""
+    import threading
+    rng = np.random.default_rng(79)
+    t = Paged(rng, [700, 65], 2, 64, 16)
+    qs = [_bf16(rng, 2, 4, 64) for _ in range(4)]
+    held = [t.pool.at(b, g, np.arange(n)) for b, n in enumerate((700, 65)) for g in range(2)]
+    before = t.cache.weights.cpu().numpy().astype(np.float64)
+    threads = [threading.Thread(target=lambda q=q: [
+        kvc.kvc_paged_decode_attention(q, t.cache, accumulate=True) for _ in range(25)]) for _, q in qs]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    torch.cuda.synchronize()
+    want, tol = before.copy(), np.zeros_like(before)
+    for q, _ in qs:
+        _, _, add, _, _, tol_add = ref.paged_decode(t.pool, q, 1 / math.sqrt(64))
+        for (b, g), a in add.items():
+            at = t.pool.at(b, g, np.arange(len(a)))
+            want[at] += 25 * a
+            tol[at] += 25 * tol_add[b, g]
+    got = t.cache.weights.cpu().numpy()
+    for at in held:  # each of the 100 sums is rounded
+        _close(got[at], want[at], tol[at] + 100 * 2.0 ** -24 * want[at] * 1.01, "weights")
+
+
 # --------------------------------------------------------------------------- #
 # bounded waits
 # --------------------------------------------------------------------------- #
