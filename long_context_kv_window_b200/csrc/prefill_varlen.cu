@@ -106,13 +106,14 @@ struct VarSmem {
 };
 
 struct VarBars {
-  uint64_t qfull, full[8], empty[8];
+  uint64_t qfull[2], full[8], empty[8];
   uint64_t s_full[2], p_full[2], o_done[2], turn[2];
   uint64_t vland[kVMaxClean], clean[kVMaxClean];  // value tiles to be checked: landed, checked (used once each)
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort, dirty, redo;
   int seq, blk;  // this CTA's sequence (-1: none) and block of it
+  int q0, k0, lq, lk;  // the sequence's first query and key, and its lengths
   float swap[2][kVT];  // [tile][row]: what the two threads of a row tell each other
 };
 
@@ -169,7 +170,7 @@ __device__ __forceinline__ int seq_blocks(const VarArgs& a, int b, bool* bad) {
   const int64_t q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
   *bad = q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k || q1 - q0 > a.max_q ||
          k1 - k0 > a.max_k;
-  return *bad ? 0 : (int)((q1 - q0 + 2 * a.nt - 1) / (2 * a.nt));
+  return *bad ? 0 : (int)(((uint32_t)(q1 - q0) + 2u * a.nt - 1u) / (2u * a.nt));
 }
 
 template <int D>
@@ -188,12 +189,12 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   const int g = (int)(blockIdx.x / (unsigned)a.splits % (unsigned)a.Hkv);
 
   if (tid == 0) {
-    tc::mbar_init(&bars->qfull, 1);
     for (int s = 0; s < L::kStages; ++s) {
       tc::mbar_init(&bars->full[s], 1);
       tc::mbar_init(&bars->empty[s], 2);
     }
     for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bars->qfull[i], 1);
       tc::mbar_init(&bars->s_full[i], 1);
       tc::mbar_init(&bars->p_full[i], 8);
       tc::mbar_init(&bars->o_done[i], 1);
@@ -237,6 +238,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       int before = 0;  // blocks of the sequences that come before this lane's
       if (a.batch <= 32) {
         const int keys = nb > 0 ? a.cu_k[lane + 1] - a.cu_k[lane] : -1;
+#pragma unroll 8
         for (int j = 0; j < a.batch; ++j) {
           const int kj = __shfl_sync(0xffffffffu, keys, j), nj = __shfl_sync(0xffffffffu, nb, j);
           if (kj > keys || (kj == keys && j < lane)) before += nj;
@@ -261,6 +263,12 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     if (lane == 0) {
       bars->seq = found;
       bars->blk = blk;
+      if (found >= 0) {
+        bars->q0 = a.cu_q[found];
+        bars->k0 = a.cu_k[found];
+        bars->lq = a.cu_q[found + 1] - bars->q0;
+        bars->lk = a.cu_k[found + 1] - bars->k0;
+      }
     }
   }
   tc::tc_fence_before();
@@ -274,15 +282,18 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   int kf = 0;      // first key of the first of them
   int q0 = 0, k0 = 0, lq = 0, lk = 0, i0 = 0;
   if (seq >= 0) {
-    q0 = a.cu_q[seq];
-    k0 = a.cu_k[seq];
-    lq = a.cu_q[seq + 1] - q0;
-    lk = a.cu_k[seq + 1] - k0;
+    q0 = bars->q0;
+    k0 = bars->k0;
+    lq = bars->lq;
+    lk = bars->lk;
     i0 = bars->blk * 2 * a.nt;
     const int lim = std::min(lq - i0, 2 * a.nt) - 1 + i0 + lk - lq;  // the last row sees keys up to here
     nt = lim >= 0 ? lim / kVT + 1 : 0;
-    const int t0 = (int)((int64_t)nt * split / a.splits);
-    nt = (int)((int64_t)nt * (split + 1) / a.splits) - t0;
+    int t0 = 0;
+    if (a.splits > 1) {
+      t0 = (int)((int64_t)nt * split / a.splits);
+      nt = (int)((int64_t)nt * (split + 1) / a.splits) - t0;
+    }
     t_mask = std::max(0, std::max(0, i0 + lk - lq + 1) / kVT - t0);
     kf = t0 * kVT;
   }
@@ -301,14 +312,14 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
-      // ---- producer: Q, then K(0), V(0), K(1), V(1), ... (pass 1: K alone)
-      if (lane == 0 && nt > 0) {
-        tc::mbar_arrive_expect_tx(&bars->qfull, (uint32_t)(2 * kCB * a.nt * a.G * 128));
-        for (int i = 0; i < 2; ++i)
-          for (int cb = 0; cb < kCB; ++cb)
-            tc::tma_load_3d(sm + i * L::kTile + cb * L::kBlk, &qmap, &bars->qfull, cb * 64, g * a.G,
-                            q0 + i0 + i * a.nt);
-      }
+      // ---- producer: Q of tile 0, K(0), Q of tile 1, then V(0), K(1), V(1), ... (pass 1: K alone)
+      auto load_q = [&](int i) {
+        tc::mbar_arrive_expect_tx(&bars->qfull[i], (uint32_t)(kCB * a.nt * a.G * 128));
+        for (int cb = 0; cb < kCB; ++cb)
+          tc::tma_load_3d(sm + i * L::kTile + cb * L::kBlk, &qmap, &bars->qfull[i], cb * 64, g * a.G,
+                          q0 + i0 + i * a.nt);
+      };
+      if (lane == 0 && nt > 0) load_q(0);
       for (int pass = 0; pass == 0 || again(pass - 1); ++pass) {
         const int count = lane != 0 ? 0 : pass == 1 ? nt : 2 * nt;
         last_pass = pass;
@@ -325,6 +336,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           for (int cb = 0; cb < kCB; ++cb)
             tc::tma_load_3d(sm + L::kRing + s * L::kTile + cb * L::kBlk, value ? &vmap : &kmap, land, cb * 64, g,
                             k0 + kf + t * kVT);
+          if (issued == 0) load_q(1);
         }
         __syncwarp();
       }
@@ -369,7 +381,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         if (nt == 0) continue;
         const int base = ring_base(pass);
         const bool maxes = pass == 1;
-        bool ok = (pass > 0 || tc::mbar_wait(&bars->qfull, 0, abort_flag)) && wait_full(base) && my_turn();
+        bool ok = (pass > 0 || tc::mbar_wait(&bars->qfull[i], 0, abort_flag)) && wait_full(base) && my_turn();
         if (ok) {
           tc::tc_fence_after();
           logits(base % L::kStages);
@@ -547,9 +559,10 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       const bool seen = limit >= kf && nt > 0;  // no key of this CTA otherwise
       const float inv = seen ? 1.f / sum_row : 0.f;
       const bool dirty = *(volatile int*)&bars->dirty != 0;
-      uint8_t* stage = sm + L::kRing + (warp - 4) * 32 * 80;  // this warp's rows
+      constexpr int kCols = D / 2, kPitch = kCols * 2 + 16;  // columns of this thread; bytes of a staged row
+      uint8_t* stage = sm + L::kRing + (warp - 4) * 32 * kPitch;  // this warp's rows
 #pragma unroll 1
-      for (int c0 = 0; c0 < D / 2; c0 += 32) {
+      for (int c0 = 0; c0 < kCols; c0 += 32) {
         uint32_t o[32];
         if (nt > 0) {
           KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
@@ -559,7 +572,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         float f[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) f[e] = seen ? __uint_as_float(o[e]) * inv : 0.f;
-        const int col = (D / 2) * hf + c0;
+        const int col = kCols * hf + c0;
         if (dirty && mine)  // non-finite values of the checked tiles, where this row sees them
           for (int j = kf + t_mask * kVT; j <= limit && j < kf + nt * kVT; ++j) {
             const uint16_t* vr = a.v + (int64_t)(k0 + j) * a.v_sn + (int64_t)g * a.v_sh + col;
@@ -576,8 +589,6 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             for (int u = 0; u < 8; ++u) po[u] = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
           continue;
         }
-        // through the ring (free now, 80-byte rows), so that a store covers 64
-        // bytes of 8 rows instead of 16 bytes of 32
 #pragma unroll
         for (int v8 = 0; v8 < 4; ++v8) {
           uint32_t w[4];
@@ -586,20 +597,29 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             const __nv_bfloat162 hp = __floats2bfloat162_rn(f[8 * v8 + 2 * u], f[8 * v8 + 2 * u + 1]);
             w[u] = *reinterpret_cast<const uint32_t*>(&hp);
           }
-          *reinterpret_cast<uint4*>(stage + lane * 80 + v8 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(stage + lane * kPitch + c0 * 2 + v8 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+      }
+      if (a.out && !a.part_o) {
+        // through the ring (free now), so that a store covers whole lines of a
+        // few rows instead of 16 bytes of 32
         __syncwarp();
+        constexpr int kPer = kCols / 8, kAt = 32 / kPer;  // lanes per row, rows per store
+        const int rel = mine ? ti * a.H + h : -1, piece = lane % kPer;
+        uint16_t* base = a.out + (int64_t)(q0 + i0) * a.H * D + kCols * hf + piece * 8;
 #pragma unroll
-        for (int k8 = 0; k8 < 4; ++k8) {
-          const int src = 8 * k8 + (lane >> 2);
-          const int64_t at = __shfl_sync(0xffffffffu, mine ? (row * a.H + h) * D : -1, src);
-          const uint4 y = *reinterpret_cast<const uint4*>(stage + src * 80 + (lane & 3) * 16);
-          if (at >= 0) *reinterpret_cast<uint4*>(a.out + at + col + (lane & 3) * 8) = y;
+        for (int k = 0; k < 32 / kAt; ++k) {
+          const int src = kAt * k + lane / kPer;
+          const int at = __shfl_sync(0xffffffffu, rel, src);
+          const uint4 y = *reinterpret_cast<const uint4*>(stage + src * kPitch + piece * 16);
+          if (at >= 0) *reinterpret_cast<uint4*>(base + (int64_t)at * D) = y;
         }
-        __syncwarp();
       }
       if (mine && hf == 0) {
-        const double z = (double)m_ref + log2((double)sum_row);
+        // m_ref + log2(sum), the logarithm from the sum's mantissa and exponent
+        int e2;
+        const float f2 = frexpf(sum_row, &e2);
+        const double z = (double)m_ref + ((double)e2 + (double)log2f(f2));
         if (a.part_z)
           a.part_z[((int64_t)split * a.total_q + row) * a.H + h] = seen ? (float)z : -INFINITY;
         else if (a.lse)
@@ -611,7 +631,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   __syncthreads();
   if (*abort_flag && tid == 0) {
     set_dev_err(a.err, KVC_DEV_ERR_TIMEOUT);
-    if (issued > 0) tc::mbar_drain(&bars->qfull, 0);
+    for (int i = 0; issued > 0 && i < 2; ++i) tc::mbar_drain(&bars->qfull[i], 0);
     for (int j = std::max(0, issued - L::kStages); j < issued; ++j)
       tc::mbar_drain(&bars->full[j % L::kStages], (j / L::kStages) & 1);
     for (int t = t_mask; last_pass != 1 && t < nt; ++t)
