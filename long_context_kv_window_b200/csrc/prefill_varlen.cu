@@ -30,14 +30,22 @@
 //
 // P overwrites the logits it came from (the TMEM has room for a second buffer
 // only with 80-key tiles, where the narrower MMAs cost more than the overlap
-// gives: 32K tokens 8.4 ms against 7.9), so logits, softmax and output of an MMA tile follow one another, and
-// while one tile is at the tensor core the other is at its softmax.  Two
-// threads per row halve the time the softmax takes.
+// gives: 32K tokens 8.4 ms against 7.9), so logits, softmax and output of an
+// MMA tile follow one another, and while one tile is at the tensor core the
+// other is at its softmax.  Two threads per row halve the time the softmax
+// takes.
+//
+// A CTA goes on to blocks of CTAs of the grid that have not started
+// (clusterlaunchcontrol): the next block is found, and its Q and first key
+// tiles land, while the softmax warps store the output of the one before.
+// What a block costs beside its key tiles went from 9.7 to 6.2 us (about 3.5
+// tiles: the first tile's way through, the last one's, the stores), of a
+// batch of 512 from 14 to 7.
 //
 // Measured (32/8 heads, d = 128): 32K tokens 6.9 ms in bursts (1.27 PFLOP/s, 75 %
-// of the measured burst rate of a library GEMM), 7.9 to 8.1 ms for seconds on end
-// (1.1 PFLOP/s, 79 % of the sustained rate; the board's power bounds it: SM clock
-// 1.55 GHz).  A key tile takes 3400 cycles of 2048 that its MMAs need: per MMA
+// of the measured burst rate of a library GEMM), 7.8 to 7.9 ms for seconds on end
+// (1.12 PFLOP/s, 80 % of the sustained rate; the board's power bounds it: SM clock
+// 1.55 GHz); 8 prompts of 1K to 8K 1.55 ms; 512 prompts of 64 tokens 240 us.  A key tile takes 3400 cycles of 2048 that its MMAs need: per MMA
 // tile the softmax 1700 (1450 of them the exponentials, 1024 at the MUFU's rate)
 // and MMAs with their hand-overs 1700.  Tried: a part of the exponentials on the
 // FMA pipe as polynomials (1/8: 3 %, 1/2: 10 % slower: more instructions, more
@@ -50,8 +58,8 @@
 // row of the block masks a key are looked over first, infinities and NaN in
 // them are set to 0, and the rows that do see such a value add it at the end.
 //
-// Warps: 0 TMA producer, 1 and 2 MMA issuers of tiles 0 and 1 (1: TMEM), 3 value
-// check, 4..11 and 12..19 the softmax of tiles 0 and 1.  Every wait is
+// Warps: 0 TMA producer, 1 and 2 MMA issuers of tiles 0 and 1 (1: TMEM), 3 the
+// next block and the value check, 4..11 and 12..19 the softmax of tiles 0 and 1.  Every wait is
 // bounded; on a timeout the CTA records KVC_DEV_ERR_TIMEOUT, lets its copies
 // and MMAs land, frees TMEM and exits.
 #include <cuda.h>
@@ -105,17 +113,54 @@ struct VarSmem {
   static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
 
+// A block of queries as a CTA computes it, found while the block before runs.
+struct VarBlk {
+  int seq;             // -1: no more blocks
+  int g, split;        // KV head, split
+  int q0, k0, lq, lk;  // first query and key of the sequence, and its lengths
+  int i0;              // first query of the block in the sequence
+  int nt, t_mask, kf;  // key tiles; first of them in which some row masks a key; first key of the first
+  int dirty, redo;     // a checked tile holds infinities or NaN; some row passed its reference by too much
+  int stop[3];         // by pass: a wait of some thread gave up
+};
+
 struct VarBars {
   uint64_t qfull[2], full[8], empty[8];
   uint64_t s_full[2], p_full[2], o_done[2], turn[2];
-  uint64_t vland[kVMaxClean], clean[kVMaxClean];  // value tiles to be checked: landed, checked (used once each)
+  uint64_t vland[kVMaxClean], clean[kVMaxClean];  // value tiles to be checked, in turn: landed, checked
+  uint64_t stored;   // the output rows of a block have left the ring
+  uint64_t claimed;  // the next CTA of the grid was asked for
   uint64_t mma_done;
+  uint4 claim;
   uint32_t tmem_base;
-  int abort, dirty, redo;
-  int seq, blk;  // this CTA's sequence (-1: none) and block of it
-  int q0, k0, lq, lk;  // the sequence's first query and key, and its lengths
+  int abort;
+  int land[8];  // by stage: the checked tile that was requested into it, or -1
+  VarBlk blk[3];
   float swap[2][kVT];  // [tile][row]: what the two threads of a row tell each other
 };
+
+// Takes over a CTA of the grid that has not started, if there is one: its index
+// lands in *claim with 16 bytes on `bar`.
+__device__ __forceinline__ void claim_cta(uint4* claim, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   tc::smem_u32(claim)),
+               "r"(tc::smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ int claimed_cta(const uint4* claim) {  // its blockIdx.x, or -1
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(tc::smem_u32(claim))
+      : "memory");
+  return got ? (int)x : -1;
+}
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -185,8 +230,6 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   VarBars* bars = reinterpret_cast<VarBars*>(sm + L::kBarOff);
   static_assert(sizeof(VarBars) <= kVBarBytes, "barrier block");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = (int)(blockIdx.x % (unsigned)a.splits);  // the splits of a block side by side, then its heads
-  const int g = (int)(blockIdx.x / (unsigned)a.splits % (unsigned)a.Hkv);
 
   if (tid == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -204,10 +247,10 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       tc::mbar_init(&bars->vland[i], 1);
       tc::mbar_init(&bars->clean[i], 1);
     }
+    tc::mbar_init(&bars->stored, 16);
+    tc::mbar_init(&bars->claimed, 1);
     tc::mbar_init(&bars->mma_done, 2);
     bars->abort = 0;
-    bars->dirty = 0;
-    bars->redo = 0;
     tc::fence_mbar_init();
     tc::prefetch_tmap(&qmap);
     tc::prefetch_tmap(&kmap);
@@ -224,121 +267,166 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   }
   tc::fence_proxy_async_smem();
   pdl_wait();  // the inputs may come from the previous kernel of the stream
-  if (warp == 2) {
-    // the block of this CTA: up to 32 sequences the longest first, more in
-    // order; the last (longest) block of each first.  Four chunks of 512
-    // queries over 8K to 32K keys: 1010 us in order, 836 us sorted.  The
-    // first CTA looks at every sequence, for the error word.
-    const bool first = blockIdx.x == 0;
-    int left = (int)(blockIdx.x / (unsigned)a.splits / (unsigned)a.Hkv), found = -1, blk = 0;
-    for (int b0 = 0; b0 < a.batch && (found < 0 || first); b0 += 32) {
-      bool bad = false;
-      const int nb = b0 + lane < a.batch ? seq_blocks(a, b0 + lane, &bad) : 0;
-      if (bad && first) set_dev_err(a.err, KVC_DEV_ERR_SEQLENS);
-      int before = 0;  // blocks of the sequences that come before this lane's
-      if (a.batch <= 32) {
-        const int keys = nb > 0 ? a.cu_k[lane + 1] - a.cu_k[lane] : -1;
+  // The block of CTA `item` of the grid, by a warp: the splits of a block side by
+  // side, then its heads, then the blocks, the last (longest) of a sequence
+  // first; up to 32 sequences the longest first, more in order.  Four chunks of
+  // 512 queries over 8K to 32K keys: 1010 us in order, 836 us sorted.
+  // It looks at 32 sequences, one per lane, and keeps them for the next search.
+  int cur_b = 0, cur_before = 0, cur_blocks = 0;  // the first of them, blocks before it, their blocks
+  int c_nb = 0, c_before = 0, c_q0 = 0, c_k0 = 0, c_lq = 0, c_lk = 0;  // the lane's: blocks, blocks of them before it
+  auto read_sequences = [&]() {
+    const int b = cur_b + lane;
+    c_nb = 0;
+    if (b < a.batch) {
+      bool bad;
+      c_nb = seq_blocks(a, b, &bad);
+      c_q0 = a.cu_q[b];
+      c_k0 = a.cu_k[b];
+      c_lq = a.cu_q[b + 1] - c_q0;
+      c_lk = a.cu_k[b + 1] - c_k0;
+    }
+    if (a.batch <= 32) {
+      const int keys = c_nb > 0 ? c_lk : -1;
+      c_before = 0;
 #pragma unroll 8
-        for (int j = 0; j < a.batch; ++j) {
-          const int kj = __shfl_sync(0xffffffffu, keys, j), nj = __shfl_sync(0xffffffffu, nb, j);
-          if (kj > keys || (kj == keys && j < lane)) before += nj;
-        }
-      } else {
-        int inc = nb;
+      for (int j = 0; j < a.batch; ++j) {
+        const int kj = __shfl_sync(0xffffffffu, keys, j), nj = __shfl_sync(0xffffffffu, c_nb, j);
+        if (kj > keys || (kj == keys && j < lane)) c_before += nj;
+      }
+    } else {
+      int inc = c_nb;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      c_before = inc - c_nb;
+    }
+    cur_blocks = __reduce_add_sync(0xffffffffu, c_nb);
+  };
+  auto find = [&](int item, VarBlk* out) {
+    const unsigned at = (unsigned)item / (unsigned)a.splits;
+    const int block = (int)(at / (unsigned)a.Hkv);
+    if (item >= 0) {
+      if (block < cur_before) {
+        cur_b = cur_before = 0;
+        read_sequences();
+      }
+      while (block >= cur_before + cur_blocks && cur_b + 32 < a.batch) {
+        cur_before += cur_blocks;
+        cur_b += 32;
+        read_sequences();
+      }
+    }
+    const int left = block - cur_before;
+    const unsigned hit = __ballot_sync(0xffffffffu, item >= 0 && left >= c_before && left < c_before + c_nb);
+    const bool mine = hit ? lane == __ffs(hit) - 1 : lane == 0;  // the lane that has the sequence
+    if (mine) {
+      VarBlk b{};
+      b.seq = hit ? cur_b + lane : -1;
+      if (hit) {
+        b.split = item % a.splits;
+        b.g = (int)(at % (unsigned)a.Hkv);
+        b.q0 = c_q0;
+        b.k0 = c_k0;
+        b.lq = c_lq;
+        b.lk = c_lk;
+        b.i0 = (c_nb - 1 - (left - c_before)) * 2 * a.nt;
+        const int lim = std::min(b.lq - b.i0, 2 * a.nt) - 1 + b.i0 + b.lk - b.lq;  // the last row sees keys up to here
+        int t0 = 0;
+        b.nt = lim >= 0 ? lim / kVT + 1 : 0;
+        if (a.splits > 1) {
+          t0 = (int)((int64_t)b.nt * b.split / a.splits);
+          b.nt = (int)((int64_t)b.nt * (b.split + 1) / a.splits) - t0;
         }
-        before = inc - nb;
+        b.t_mask = std::max(0, std::max(0, b.i0 + b.lk - b.lq + 1) / kVT - t0);
+        b.kf = t0 * kVT;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, left >= before && left < before + nb);
-      if (hit && found < 0) {
-        const int src = __ffs(hit) - 1;
-        found = b0 + src;
-        blk = __shfl_sync(0xffffffffu, nb, src) - 1 - (left - __shfl_sync(0xffffffffu, before, src));
-      }
-      left -= __reduce_add_sync(0xffffffffu, nb);
+      *out = b;
     }
-    if (lane == 0) {
-      bars->seq = found;
-      bars->blk = blk;
-      if (found >= 0) {
-        bars->q0 = a.cu_q[found];
-        bars->k0 = a.cu_k[found];
-        bars->lq = a.cu_q[found + 1] - bars->q0;
-        bars->lk = a.cu_k[found + 1] - bars->k0;
-      }
-    }
+    __syncwarp();
+  };
+  if (warp == 3) {
+    read_sequences();
+    find((int)blockIdx.x, &bars->blk[0]);
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort;
-  const int seq = bars->seq;
-  int nt = 0;      // key tiles of this CTA: up to the block's last row, or its share of them
-  int t_mask = 0;  // first of them in which some row of the block masks a key
-  int kf = 0;      // first key of the first of them
-  int q0 = 0, k0 = 0, lq = 0, lk = 0, i0 = 0;
-  if (seq >= 0) {
-    q0 = bars->q0;
-    k0 = bars->k0;
-    lq = bars->lq;
-    lk = bars->lk;
-    i0 = bars->blk * 2 * a.nt;
-    const int lim = std::min(lq - i0, 2 * a.nt) - 1 + i0 + lk - lq;  // the last row sees keys up to here
-    nt = lim >= 0 ? lim / kVT + 1 : 0;
-    int t0 = 0;
-    if (a.splits > 1) {
-      t0 = (int)((int64_t)nt * split / a.splits);
-      nt = (int)((int64_t)nt * (split + 1) / a.splits) - t0;
-    }
-    t_mask = std::max(0, std::max(0, i0 + lk - lq + 1) / kVT - t0);
-    kf = t0 * kVT;
-  }
-  int issued = 0, last_pass = 0;  // producer: K and V tiles requested
-  // Pass 0 computes; if a row passed its reference by too much, pass 1 finds
-  // every row's max and pass 2 computes with that of the rows that did.  The ring and the barriers
-  // go on counting from pass to pass.
-  auto again = [&](int pass) {
+  // The CTA goes from block to block.  Ring and barriers go on counting
+  // from block to block, and from pass to pass of a block: pass 0 computes; if
+  // a row passed its reference by too much, pass 1 finds every row's max and
+  // pass 2 computes with that of the rows that did.
+  int n3 = 0;         // the block's number, modulo 3
+  int ring0 = 0;      // K and V tiles of the blocks and passes before
+  int checks = 0;     // of them the checked ones
+  int tiles = 0;      // logits tiles of the blocks and passes before
+  bool quit = bars->blk[0].seq < 0;
+  // ends a pass; whether the block needs another.  What every thread decides
+  // by is written before the barrier and not after it.
+  auto again = [&](int pass, int nt, int nc) {
+    VarBlk* b = &bars->blk[n3];
+    if (*abort_flag) *(volatile int*)&b->stop[pass] = 1;
     tc::named_bar_sync(15, kVBlock);
-    if (*abort_flag) return false;
-    return pass == 0 ? *(volatile int*)&bars->redo != 0 : pass == 1;
+    ring0 += pass == 1 ? nt : 2 * nt;
+    tiles += nt;
+    if (pass != 1) checks += nc;
+    if (*(volatile int*)&b->stop[pass]) {
+      quit = true;
+      return false;
+    }
+    return pass == 0 ? *(volatile int*)&b->redo != 0 : pass == 1;
   };
-  auto ring_base = [&](int pass) { return pass == 0 ? 0 : pass == 1 ? 2 * nt : 3 * nt; };
+  auto next_block = [&]() {
+    n3 = n3 == 2 ? 0 : n3 + 1;
+    if (!quit) quit = *(volatile int*)&bars->blk[n3].seq < 0;
+  };
+  int issued = 0;           // producer: K and V tiles requested
+  int q_loads[2] = {0, 0};  // and Q tiles
 
   // registers: 640 x 96 at launch; the softmax warps take over what the others do not need
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
       // ---- producer: Q of tile 0, K(0), Q of tile 1, then V(0), K(1), V(1), ... (pass 1: K alone)
-      auto load_q = [&](int i) {
-        tc::mbar_arrive_expect_tx(&bars->qfull[i], (uint32_t)(kCB * a.nt * a.G * 128));
-        for (int cb = 0; cb < kCB; ++cb)
-          tc::tma_load_3d(sm + i * L::kTile + cb * L::kBlk, &qmap, &bars->qfull[i], cb * 64, g * a.G,
-                          q0 + i0 + i * a.nt);
-      };
-      if (lane == 0 && nt > 0) load_q(0);
-      for (int pass = 0; pass == 0 || again(pass - 1); ++pass) {
-        const int count = lane != 0 ? 0 : pass == 1 ? nt : 2 * nt;
-        last_pass = pass;
-        for (int j = 0; j < count; ++j, ++issued) {
-          const int s = issued % L::kStages;
-          if (issued >= L::kStages && !tc::mbar_wait(&bars->empty[s], ((issued / L::kStages) - 1) & 1, abort_flag)) break;
-          // a value tile to be checked lands on a barrier of its own, which its
-          // readers can wait for without following the ring's phases
-          const int t = pass == 1 ? j : j >> 1;
-          const bool value = pass != 1 && (j & 1), checked = value && t >= t_mask;
-          uint64_t* land = checked ? &bars->vland[t - t_mask] : &bars->full[s];
-          if (checked) tc::mbar_arrive(&bars->full[s]);
-          tc::mbar_arrive_expect_tx(land, (uint32_t)L::kTile);
+      for (int n = 0; !quit; ++n, next_block()) {
+        const VarBlk b = bars->blk[n3];
+        const int nc = std::max(0, b.nt - b.t_mask), first = issued;
+        auto load_q = [&](int i) {
+          tc::mbar_arrive_expect_tx(&bars->qfull[i], (uint32_t)(kCB * a.nt * a.G * 128));
           for (int cb = 0; cb < kCB; ++cb)
-            tc::tma_load_3d(sm + L::kRing + s * L::kTile + cb * L::kBlk, value ? &vmap : &kmap, land, cb * 64, g,
-                            k0 + kf + t * kVT);
-          if (issued == 0) load_q(1);
+            tc::tma_load_3d(sm + i * L::kTile + cb * L::kBlk, &qmap, &bars->qfull[i], cb * 64, b.g * a.G,
+                            b.q0 + b.i0 + i * a.nt);
+          ++q_loads[i];
+        };
+        if (lane == 0 && b.nt > 0) load_q(0);
+        for (int pass = 0; pass == 0 || again(pass - 1, b.nt, nc); ++pass) {
+          const int count = lane != 0 ? 0 : pass == 1 ? b.nt : 2 * b.nt;
+          for (int j = 0; j < count; ++j, ++issued) {
+            const int s = issued % L::kStages;
+            if (issued >= L::kStages && !tc::mbar_wait(&bars->empty[s], ((issued / L::kStages) - 1) & 1, abort_flag))
+              break;
+            // the two stages before the block's first hold output rows of the block before
+            if (n > 0 && issued == first + L::kStages - 2 && !tc::mbar_wait(&bars->stored, (n - 1) & 1, abort_flag))
+              break;
+            // a value tile to be checked lands on a barrier of its own, which its
+            // readers can wait for without following the ring's phases
+            const int t = pass == 1 ? j : j >> 1;
+            const bool value = pass != 1 && (j & 1), checked = value && t >= b.t_mask;
+            const int c = checks + t - b.t_mask;
+            uint64_t* land = checked ? &bars->vland[c % kVMaxClean] : &bars->full[s];
+            bars->land[s] = checked ? c : -1;
+            if (checked) tc::mbar_arrive(&bars->full[s]);
+            tc::mbar_arrive_expect_tx(land, (uint32_t)L::kTile);
+            for (int cb = 0; cb < kCB; ++cb)
+              tc::tma_load_3d(sm + L::kRing + s * L::kTile + cb * L::kBlk, value ? &vmap : &kmap, land, cb * 64, b.g,
+                              b.k0 + b.kf + t * kVT);
+            if (issued == first) load_q(1);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     } else if (warp < 3) {
       // ---- MMA issuers, one per MMA tile: S of key tile 0, then for every key
@@ -377,78 +465,119 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         commit(&bars->s_full[i]);
       };
       auto wait_full = [&](int j) { return tc::mbar_wait(&bars->full[j % L::kStages], (j / L::kStages) & 1, abort_flag); };
-      for (int pass = 0; pass == 0 || again(pass - 1); ++pass) {
-        if (nt == 0) continue;
-        const int base = ring_base(pass);
-        const bool maxes = pass == 1;
-        bool ok = (pass > 0 || tc::mbar_wait(&bars->qfull[i], 0, abort_flag)) && wait_full(base) && my_turn();
-        if (ok) {
-          tc::tc_fence_after();
-          logits(base % L::kStages);
-        }
-        for (int t = 0; ok && t < nt; ++t) {
-          const int vj = base + 2 * t + 1, vs = vj % L::kStages;               // V(t)
-          const int kj = maxes ? base + t + 1 : vj + 1, ks_ = kj % L::kStages;  // K(t + 1)
-          if (!maxes) {
-            ok = wait_full(vj);
-            if (ok && t >= t_mask) ok = tc::mbar_wait(&bars->clean[t - t_mask], pass >> 1, abort_flag);
+      for (int qn = 0; !quit; next_block()) {
+        const int nt = bars->blk[n3].nt, t_mask = bars->blk[n3].t_mask, nc = std::max(0, nt - t_mask);
+        for (int pass = 0; pass == 0 || again(pass - 1, nt, nc); ++pass) {
+          if (nt == 0) continue;
+          const int base = ring0;
+          const bool maxes = pass == 1;
+          bool ok = (pass > 0 || tc::mbar_wait(&bars->qfull[i], qn++ & 1, abort_flag)) && wait_full(base) && my_turn();
+          if (ok) {
+            tc::tc_fence_after();
+            logits(base % L::kStages);
           }
-          if (ok && t + 1 < nt) ok = wait_full(kj);
-          if (ok) ok = tc::mbar_wait(&bars->p_full[i], (pass * nt + t) & 1, abort_flag);
-          if (ok) ok = my_turn();
-          if (!ok) break;
-          tc::tc_fence_after();
-          if (!maxes) {
-            const uint64_t vd = v_desc + (uint64_t)((uint32_t)(vs * L::kTile) >> 4);
+          for (int t = 0; ok && t < nt; ++t) {
+            const int vj = base + 2 * t + 1, vs = vj % L::kStages;               // V(t)
+            const int kj = maxes ? base + t + 1 : vj + 1, ks_ = kj % L::kStages;  // K(t + 1)
+            if (!maxes) {
+              ok = wait_full(vj);
+              const int c = checks + t - t_mask;
+              if (ok && t >= t_mask) ok = tc::mbar_wait(&bars->clean[c % kVMaxClean], (c / kVMaxClean) & 1, abort_flag);
+            }
+            if (ok && t + 1 < nt) ok = wait_full(kj);
+            if (ok) ok = tc::mbar_wait(&bars->p_full[i], (tiles + t) & 1, abort_flag);
+            if (ok) ok = my_turn();
+            if (!ok) break;
+            tc::tc_fence_after();
+            if (!maxes) {
+              const uint64_t vd = v_desc + (uint64_t)((uint32_t)(vs * L::kTile) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)  // 16 keys: 8 columns of P (64 keys over each half of S), 16 value rows of 128 B
-              if (elect_one())
-                mma_bf16_ts(o_tmem, s_tmem + (uint32_t)(64 * (ks >> 2) + 8 * (ks & 3)),
-                            vd + (uint64_t)((uint32_t)(ks * 16 * 128) >> 4), id_o, (t > 0 || ks > 0) ? 1u : 0u);
-          }
-          if (t + 1 < nt) {
-            logits(ks_);
-          } else {
-            your_turn();
-            if (!maxes) commit(&bars->o_done[i]);
+              for (int ks = 0; ks < 8; ++ks)  // 16 keys: 8 columns of P (64 keys over each half of S), 16 value rows of 128 B
+                if (elect_one())
+                  mma_bf16_ts(o_tmem, s_tmem + (uint32_t)(64 * (ks >> 2) + 8 * (ks & 3)),
+                              vd + (uint64_t)((uint32_t)(ks * 16 * 128) >> 4), id_o, (t > 0 || ks > 0) ? 1u : 0u);
+            }
+            if (t + 1 < nt) {
+              logits(ks_);
+            } else {
+              your_turn();
+              if (!maxes) commit(&bars->o_done[i]);
+            }
           }
         }
       }
       commit(&bars->mma_done);  // every MMA issued above has completed before TMEM is freed
       tc::mbar_drain(&bars->mma_done, 0);
     } else {
-      // ---- value check: the tiles in which some row masks a key
+      // ---- value check: the tiles in which some row masks a key; and the next block
       constexpr int kVec = L::kTile / 16;
-      for (int pass = 0; pass == 0 || again(pass - 1); ++pass) {
-        if (pass == 1) continue;
-        for (int t = t_mask; t < nt; ++t) {
-          const int s = (ring_base(pass) + 2 * t + 1) % L::kStages;
-          if (!tc::mbar_wait(&bars->vland[t - t_mask], pass >> 1, abort_flag)) break;
-          uint4* tile = reinterpret_cast<uint4*>(sm + L::kRing + s * L::kTile);
-          uint32_t top = 0;  // the largest magnitude, per 16-bit half
-#pragma unroll 8
-          for (int i = lane; i < kVec; i += 32) {
-            const uint4 w = tile[i];
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                         __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
-          }
-          if ((top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u) {
-            bars->dirty = 1;
-            for (int i = lane; i < kVec; i += 32) {
-              uint32_t* w = reinterpret_cast<uint32_t*>(tile + i);
-              for (int u = 0; u < 4; ++u) {
-                uint32_t x = w[u];
-                if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
-                if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
-                w[u] = x;
-              }
-            }
-            tc::fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bars->clean[t - t_mask]);
+      auto look = [&]() {
+        for (int b = lane; b < a.batch; b += 32) {
+          bool bad;
+          seq_blocks(a, b, &bad);
+          if (bad) set_dev_err(a.err, KVC_DEV_ERR_SEQLENS);
         }
+      };
+      int claims = 0;
+      bool scan = blockIdx.x == 0;  // by whoever computes item 0: every sequence is looked at, for the error word
+      for (; !quit; next_block()) {
+        const int nt = bars->blk[n3].nt, t_mask = bars->blk[n3].t_mask, nc = std::max(0, nt - t_mask);
+        bool first = false;
+        auto find_next = [&]() {
+          const bool got = tc::mbar_wait(&bars->claimed, claims++ & 1, abort_flag);
+          const int item = __shfl_sync(0xffffffffu, got ? claimed_cta(&bars->claim) : -1, 0);
+          find(item, &bars->blk[n3 == 2 ? 0 : n3 + 1]);
+          first = item == 0;
+        };
+        for (int pass = 0; pass == 0 || again(pass - 1, nt, nc); ++pass) {
+          if (pass == 1) continue;
+          if (pass == 0) {
+            // The next block is claimed when the first of the tiles to be checked,
+            // the last ones of a block, has landed: early enough, and not so early
+            // that a CTA with a long block takes one from those that end sooner.
+            if (nc > 0) tc::mbar_wait(&bars->vland[checks % kVMaxClean], (checks / kVMaxClean) & 1, abort_flag);
+            __syncwarp();
+            if (lane == 0) {
+              tc::fence_proxy_async_smem();  // the last answer is read
+              tc::mbar_arrive_expect_tx(&bars->claimed, 16u);
+              claim_cta(&bars->claim, &bars->claimed);
+            }
+            __syncwarp();
+          }
+          for (int t = t_mask; t < nt; ++t) {
+            const int s = (ring0 + 2 * t + 1) % L::kStages, c = checks + t - t_mask;
+            if (!tc::mbar_wait(&bars->vland[c % kVMaxClean], (c / kVMaxClean) & 1, abort_flag)) break;
+            uint4* tile = reinterpret_cast<uint4*>(sm + L::kRing + s * L::kTile);
+            uint32_t top = 0;  // the largest magnitude, per 16-bit half
+#pragma unroll 8
+            for (int i = lane; i < kVec; i += 32) {
+              const uint4 w = tile[i];
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                           __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+            }
+            if ((top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u) {
+              bars->blk[n3].dirty = 1;
+              for (int i = lane; i < kVec; i += 32) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(tile + i);
+                for (int u = 0; u < 4; ++u) {
+                  uint32_t x = w[u];
+                  if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+                  if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
+                  w[u] = x;
+                }
+              }
+              tc::fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars->clean[c % kVMaxClean]);
+          }
+          if (pass == 0) find_next();
+        }
+        if (scan) look();
+        scan = first;
       }
+      if (scan) look();
+      if (lane == 0 && claims > 0) tc::mbar_drain(&bars->claimed, (claims - 1) & 1);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
@@ -457,10 +586,6 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     const int i = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, wq = warp & 3;
     const int r = 32 * wq + lane;
     const int ti = i * a.nt + r / a.G;  // token of this row in the block
-    const int h = g * a.G + r % a.G;
-    const bool mine = seq >= 0 && r < a.nt * a.G && ti < lq - i0;
-    const int limit = std::min(ti, lq - i0 - 1) + i0 + lk - lq;  // last key the row sees
-    const int64_t row = (int64_t)(q0 + i0) + ti;                 // its row of out and lse
     const uint32_t lane_base = tmem + ((uint32_t)(32 * wq) << 16);
     const uint32_t s_col = lane_base + (uint32_t)(128 * i + 64 * hf), o_col = lane_base + kO + (uint32_t)(D * i + (D / 2) * hf);
     const int pair_bar = 1 + 4 * i + wq;  // named barrier of the two warps that share these rows
@@ -474,10 +599,6 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       return hf ? *swap : mine_x;
     };
     auto larger = [](float x0, float x1) { return fmaxf(x0, x1); };
-    float m_ref = -INFINITY, top = -INFINITY;
-    bool past = false;  // the row needs its maximum as reference
-    double l = 0.0;  // this thread's half of the row sum
-    bool ok = true;
     uint32_t x[64];
     auto row_max = [&]() {  // of this thread's logits, in log2 units
       float mx[4];
@@ -488,142 +609,170 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
     };
     const bool releases = wq == 0 && hf == 0 && lane == 0;  // tells the producer for this tile
-    for (int pass = 0; pass == 0 || again(pass - 1); ++pass) {
-      const int ub = pass * nt, base = ring_base(pass);
-      l = 0.0;
-      for (int t = 0; t < nt; ++t) {
-        if (!tc::mbar_wait(&bars->s_full[i], (ub + t) & 1, abort_flag)) ok = false;
-        if (releases && ok) {  // S(t) is there: K(t) and, before it, V(t - 1) are read
-          if (pass == 1) {
-            tc::mbar_arrive(&bars->empty[(base + t) % L::kStages]);
-          } else {
-            tc::mbar_arrive(&bars->empty[(base + 2 * t) % L::kStages]);
-            if (t > 0) tc::mbar_arrive(&bars->empty[(base + 2 * t - 1) % L::kStages]);
-          }
-        }
-        __syncwarp();
-        tc::tc_fence_after();
-        KVC_TMEM_LD64(s_col, x);
-        KVC_TMEM_WAIT_LD64(x);
-        if (t >= t_mask) {
-          const int lim = limit - kf - t * kVT - 64 * hf;  // the last visible column
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e > lim) x[e] = __float_as_uint(-INFINITY);
-        }
-        if (pass == 1) {
-          top = fmaxf(top, row_max());
-        } else {
-          if (pass == 0 && t == 0) {  // the first tile sets the references, if it has a logit above -inf
-            m_ref = both(row_max(), larger);
-            past = m_ref == -INFINITY && limit >= kf + kVT;
-          }
-          // a row that has seen no key yet has only x = -inf: p = 2^-inf = 0
-          const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-          const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int u = 0; u < 32; ++u) {
-            const float2 y = tc::fma2(make_float2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), c2, nm2);
-            const float2 p = make_float2(tc::ex2_approx(y.x), tc::ex2_approx(y.y));
-            sum[u & 1] = tc::add2(sum[u & 1], p);
-            const __nv_bfloat162 hp = __floats2bfloat162_rn(p.x, p.y);
-            x[u] = *reinterpret_cast<const uint32_t*>(&hp);
-          }
-          tmem_st32(s_col, *reinterpret_cast<const uint32_t(*)[32]>(x));
-          const float2 s2 = tc::add2(sum[0], sum[1]);
-          const float s = s2.x + s2.y;
-          past |= s > kVMost;
-          l += (double)s;
-          tmem_wait_st();
-        }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && ok) tc::mbar_arrive(&bars->p_full[i]);
-      }
-      if (pass == 1) {
-        // the other rows keep theirs, and their results to the last bit
-        top = both(top, larger);
-        if (both(past ? 1.f : 0.f, larger) > 0.f) m_ref = top;
-      } else {
-        if (nt > 0 && !tc::mbar_wait(&bars->o_done[i], pass >> 1, abort_flag)) ok = false;
-        if (nt > 0 && releases && ok) tc::mbar_arrive(&bars->empty[(base + 2 * nt - 1) % L::kStages]);
-        if (pass == 0 && past && mine) bars->redo = 1;
-      }
-    }
-    // ---- the output rows and log-sum-exp; the halves store a half of the columns each
-    __syncwarp();
-    const float sum_row = both((float)l, [](float x0, float x1) { return x0 + x1; });
-    if (ok && seq >= 0) {
-      tc::tc_fence_after();
-      const bool seen = limit >= kf && nt > 0;  // no key of this CTA otherwise
-      const float inv = seen ? 1.f / sum_row : 0.f;
-      const bool dirty = *(volatile int*)&bars->dirty != 0;
-      constexpr int kCols = D / 2, kPitch = kCols * 2 + 16;  // columns of this thread; bytes of a staged row
-      uint8_t* stage = sm + L::kRing + (warp - 4) * 32 * kPitch;  // this warp's rows
-#pragma unroll 1
-      for (int c0 = 0; c0 < kCols; c0 += 32) {
-        uint32_t o[32];
-        if (nt > 0) {
-          KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
-          KVC_TMEM_WAIT_LD32(o);
-        }
-        if (!a.out && !a.part_o) continue;
-        float f[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = seen ? __uint_as_float(o[e]) * inv : 0.f;
-        const int col = kCols * hf + c0;
-        if (dirty && mine)  // non-finite values of the checked tiles, where this row sees them
-          for (int j = kf + t_mask * kVT; j <= limit && j < kf + nt * kVT; ++j) {
-            const uint16_t* vr = a.v + (int64_t)(k0 + j) * a.v_sn + (int64_t)g * a.v_sh + col;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const uint32_t bits = vr[e];
-              if ((bits & 0x7F80u) == 0x7F80u) f[e] += __uint_as_float(bits << 16);
+    for (int outs = 0; !quit; next_block()) {
+      const VarBlk* b = &bars->blk[n3];
+      const int nt = b->nt, t_mask = b->t_mask;
+      auto mine = [&]() { return r < a.nt * a.G && ti < b->lq - b->i0; };
+      // the last key the row sees, counted from the first one of this thread
+      const int limit = std::min(ti, b->lq - b->i0 - 1) + b->i0 + b->lk - b->lq - b->kf - 64 * hf;
+      float m_ref = -INFINITY, top = -INFINITY;
+      bool past = false;  // the row needs its maximum as reference
+      double l = 0.0;  // this thread's half of the row sum
+      bool ok = true;
+      for (int pass = 0; pass == 0 || again(pass - 1, nt, 0); ++pass) {
+        const int base = ring0;
+        l = 0.0;
+        for (int t = 0; t < nt; ++t) {
+          if (!tc::mbar_wait(&bars->s_full[i], (tiles + t) & 1, abort_flag)) ok = false;
+          if (releases && ok) {  // S(t) is there: K(t) and, before it, V(t - 1) are read
+            if (pass == 1) {
+              tc::mbar_arrive(&bars->empty[(base + t) % L::kStages]);
+            } else {
+              tc::mbar_arrive(&bars->empty[(base + 2 * t) % L::kStages]);
+              if (t > 0) tc::mbar_arrive(&bars->empty[(base + 2 * t - 1) % L::kStages]);
             }
           }
-        if (a.part_o) {
-          float4* po = reinterpret_cast<float4*>(a.part_o + (((int64_t)split * a.total_q + row) * a.H + h) * D + col);
-          if (mine)
+          __syncwarp();
+          tc::tc_fence_after();
+          KVC_TMEM_LD64(s_col, x);
+          KVC_TMEM_WAIT_LD64(x);
+          if (t >= t_mask) {
+            const int lim = limit - t * kVT;  // the last visible column
 #pragma unroll
-            for (int u = 0; u < 8; ++u) po[u] = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
-          continue;
-        }
-#pragma unroll
-        for (int v8 = 0; v8 < 4; ++v8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const __nv_bfloat162 hp = __floats2bfloat162_rn(f[8 * v8 + 2 * u], f[8 * v8 + 2 * u + 1]);
-            w[u] = *reinterpret_cast<const uint32_t*>(&hp);
+            for (int e = 0; e < 64; ++e)
+              if (e > lim) x[e] = __float_as_uint(-INFINITY);
           }
-          *reinterpret_cast<uint4*>(stage + lane * kPitch + c0 * 2 + v8 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      if (a.out && !a.part_o) {
-        // through the ring (free now), so that a store covers whole lines of a
-        // few rows instead of 16 bytes of 32
-        __syncwarp();
-        constexpr int kPer = kCols / 8, kAt = 32 / kPer;  // lanes per row, rows per store
-        const int rel = mine ? ti * a.H + h : -1, piece = lane % kPer;
-        uint16_t* base = a.out + (int64_t)(q0 + i0) * a.H * D + kCols * hf + piece * 8;
+          if (pass == 1) {
+            top = fmaxf(top, row_max());
+          } else {
+            if (pass == 0 && t == 0) {  // the first tile sets the references, if it has a logit above -inf
+              m_ref = both(row_max(), larger);
+              past = m_ref == -INFINITY && limit >= kVT - 64 * hf;
+            }
+            // a row that has seen no key yet has only x = -inf: p = 2^-inf = 0
+            const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+            const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int k = 0; k < 32 / kAt; ++k) {
-          const int src = kAt * k + lane / kPer;
-          const int at = __shfl_sync(0xffffffffu, rel, src);
-          const uint4 y = *reinterpret_cast<const uint4*>(stage + src * kPitch + piece * 16);
-          if (at >= 0) *reinterpret_cast<uint4*>(base + (int64_t)at * D) = y;
+            for (int u = 0; u < 32; ++u) {
+              const float2 y = tc::fma2(make_float2(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), c2, nm2);
+              const float2 p = make_float2(tc::ex2_approx(y.x), tc::ex2_approx(y.y));
+              sum[u & 1] = tc::add2(sum[u & 1], p);
+              const __nv_bfloat162 hp = __floats2bfloat162_rn(p.x, p.y);
+              x[u] = *reinterpret_cast<const uint32_t*>(&hp);
+            }
+            tmem_st32(s_col, *reinterpret_cast<const uint32_t(*)[32]>(x));
+            const float2 s2 = tc::add2(sum[0], sum[1]);
+            const float s = s2.x + s2.y;
+            past |= s > kVMost;
+            l += (double)s;
+            tmem_wait_st();
+          }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0 && ok) tc::mbar_arrive(&bars->p_full[i]);
+        }
+        if (pass == 1) {
+          // the other rows keep theirs, and their results to the last bit
+          top = both(top, larger);
+          if (both(past ? 1.f : 0.f, larger) > 0.f) m_ref = top;
+        } else {
+          if (nt > 0 && !tc::mbar_wait(&bars->o_done[i], outs++ & 1, abort_flag)) ok = false;
+          if (nt > 0 && releases && ok) tc::mbar_arrive(&bars->empty[(base + 2 * nt - 1) % L::kStages]);
+          if (pass == 0 && past && mine()) bars->blk[n3].redo = 1;
         }
       }
-      if (mine && hf == 0) {
-        // m_ref + log2(sum), the logarithm from the sum's mantissa and exponent
-        int e2;
-        const float f2 = frexpf(sum_row, &e2);
-        const double z = (double)m_ref + ((double)e2 + (double)log2f(f2));
-        if (a.part_z)
-          a.part_z[((int64_t)split * a.total_q + row) * a.H + h] = seen ? (float)z : -INFINITY;
-        else if (a.lse)
-          a.lse[row * a.H + h] = seen ? (float)(z * kLn2) : -INFINITY;
+      // ---- the output rows and log-sum-exp; the halves store a half of the columns each
+      if (quit) break;
+      __syncwarp();
+      int ln = lane;  // the lane, from which nothing can be computed ahead of the loop over the blocks
+      asm volatile("" : "+r"(ln));
+      const int q0 = b->q0, k0 = b->k0, i0 = b->i0, g = b->g, h = g * a.G + r % a.G;
+      const bool own = mine();
+      const int64_t row = (int64_t)(q0 + i0) + ti;  // the row of out and lse
+      const float sum_row = both((float)l, [](float x0, float x1) { return x0 + x1; });
+      {
+        tc::tc_fence_after();
+        const bool seen = limit >= -64 * hf && nt > 0;  // no key of this CTA otherwise
+        const float inv = seen ? 1.f / sum_row : 0.f;
+        const bool dirty = *(volatile int*)&b->dirty != 0;
+        // this warp's rows, in one of the ring's two stages that are requested last: pieces of 16 bytes, swizzled
+        constexpr int kCols = D / 2, kPitch = kCols * 2;  // columns of this thread
+        uint8_t* stage = sm + L::kRing + (ring0 + L::kStages - 2 + i) % L::kStages * L::kTile + ((warp - 4) & 7) * 32 * kPitch;
+        auto piece_of = [](int row_, int piece_) {
+          return row_ * kPitch + ((piece_ ^ (D == 128 ? row_ & 7 : row_ >> 1 & 3)) << 4);
+        };
+#pragma unroll 1
+        for (int c0 = 0; c0 < kCols; c0 += 32) {
+          uint32_t o[32];
+          if (nt > 0) {
+            KVC_TMEM_LD32(o_col + (uint32_t)c0, o);
+            KVC_TMEM_WAIT_LD32(o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (!a.out && !a.part_o) continue;
+          float f[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) f[e] = seen ? __uint_as_float(o[e]) * inv : 0.f;
+          const int col = kCols * hf + c0;
+          if (dirty && own)  // non-finite values of the checked tiles, where this row sees them
+            for (int kf = b->kf, j = kf + t_mask * kVT; j <= limit + kf + 64 * hf && j < kf + nt * kVT; ++j) {
+              const uint16_t* vr = a.v + (int64_t)(k0 + j) * a.v_sn + (int64_t)g * a.v_sh + col;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t bits = vr[e];
+                if ((bits & 0x7F80u) == 0x7F80u) f[e] += __uint_as_float(bits << 16);
+              }
+            }
+          if (a.part_o) {
+            float4* po = reinterpret_cast<float4*>(a.part_o + (((int64_t)b->split * a.total_q + row) * a.H + h) * D + col);
+            if (own)
+#pragma unroll
+              for (int u = 0; u < 8; ++u) po[u] = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
+            continue;
+          }
+#pragma unroll
+          for (int v8 = 0; v8 < 4; ++v8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const __nv_bfloat162 hp = __floats2bfloat162_rn(f[8 * v8 + 2 * u], f[8 * v8 + 2 * u + 1]);
+              w[u] = *reinterpret_cast<const uint32_t*>(&hp);
+            }
+            *reinterpret_cast<uint4*>(stage + piece_of(ln, c0 / 8 + v8)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (a.out && !a.part_o) {
+          // through the ring, so that a store covers whole lines of a
+          // few rows instead of 16 bytes of 32
+          __syncwarp();
+          constexpr int kPer = kCols / 8, kAt = 32 / kPer;  // lns per row, rows per store
+          const int rel = own ? ti * a.H + h : -1, piece = ln % kPer;
+          uint16_t* base = a.out + (int64_t)(q0 + i0) * a.H * D + kCols * hf + piece * 8;
+#pragma unroll
+          for (int k = 0; k < 32 / kAt; ++k) {
+            const int src = kAt * k + ln / kPer;
+            const int at = __shfl_sync(0xffffffffu, rel, src);
+            const uint4 y = *reinterpret_cast<const uint4*>(stage + piece_of(src, piece));
+            if (at >= 0) *reinterpret_cast<uint4*>(base + (int64_t)at * D) = y;
+          }
+        }
+        if (own && hf == 0) {
+          // m_ref + log2(sum), the logarithm from the sum's mantissa and exponent
+          int e2;
+          const float f2 = frexpf(sum_row, &e2);
+          const double z = (double)m_ref + ((double)e2 + (double)log2f(f2));
+          if (a.part_z)
+            a.part_z[((int64_t)b->split * a.total_q + row) * a.H + h] = seen ? (float)z : -INFINITY;
+          else if (a.lse)
+            a.lse[row * a.H + h] = seen ? (float)(z * kLn2) : -INFINITY;
+        }
+        tc::tc_fence_before();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->stored);
       }
     }
   }
@@ -631,11 +780,15 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   __syncthreads();
   if (*abort_flag && tid == 0) {
     set_dev_err(a.err, KVC_DEV_ERR_TIMEOUT);
-    for (int i = 0; issued > 0 && i < 2; ++i) tc::mbar_drain(&bars->qfull[i], 0);
-    for (int j = std::max(0, issued - L::kStages); j < issued; ++j)
-      tc::mbar_drain(&bars->full[j % L::kStages], (j / L::kStages) & 1);
-    for (int t = t_mask; last_pass != 1 && t < nt; ++t)
-      if (issued > ring_base(last_pass) + 2 * t + 1) tc::mbar_drain(&bars->vland[t - t_mask], last_pass >> 1);
+    for (int i = 0; i < 2; ++i)
+      if (q_loads[i] > 0) tc::mbar_drain(&bars->qfull[i], (q_loads[i] - 1) & 1);
+    for (int j = std::max(0, issued - L::kStages); j < issued; ++j) {
+      const int s = j % L::kStages, c = bars->land[s];
+      if (c >= 0)
+        tc::mbar_drain(&bars->vland[c % kVMaxClean], (c / kVMaxClean) & 1);
+      else
+        tc::mbar_drain(&bars->full[s], (j / L::kStages) & 1);
+    }
   }
   if (warp == 1) {
     tc::tc_fence_after();

@@ -249,6 +249,61 @@ def test_prefill_varlen_rows_beside_one_that_outgrows_its_reference():
         assert not torch.equal(out[270:], clean[270:])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_varlen_more_blocks_than_sms(d):
+    """A CTA computes one block after another: blocks without keys, of one key
+    tile and of several, some of them computed again with the rows' maxima,
+    some with infinities among their masked values.  Every sequence comes out
+    as it does alone, and as defined."""
+    rng = np.random.default_rng(33)
+    B, H, Hkv = 90, 8, 4
+    lens_k = [int(x) for x in rng.integers(0, 420, B)]
+    lens_q = [int(rng.integers(0, n + 1)) if b % 3 else n for b, n in enumerate(lens_k)]
+    lens_q[7], lens_k[8], lens_q[8] = lens_k[7] + 40, 0, 3  # rows that see no key
+    cu_q, cu_k = np.cumsum([0] + lens_q), np.cumsum([0] + lens_k)
+    q, qd = _bf16(rng, sum(lens_q), H, d)
+    k, kd = _bf16(rng, sum(lens_k), Hkv, d)
+    v, vd = _bf16(rng, sum(lens_k), Hkv, d)
+    clean = _run_prefill(qd, kd, vd, lens_q, lens_k)
+    w_out, w_lse, tol, tol_lse = ref.prefill_varlen(q, k, v, cu_q, cu_k, 1 / math.sqrt(d))
+    _close(_np(clean[0]), w_out, tol, "out")
+    _close(_np(clean[1]), w_lse, tol_lse, "lse")
+    again = [b for b in range(B) if lens_k[b] > 200 and lens_q[b] > 150]
+    assert len(again) > 10
+    for b in again:
+        at = cu_k[b + 1] - 20
+        if b % 2:
+            kd[at] = 90.0  # lifts the rows behind it by far, where q sums to more than 0
+        else:
+            vd[at] = float("inf")
+    graph, out, lse = torch.cuda.CUDAGraph(), torch.zeros_like(clean[0]), torch.zeros_like(clean[1])
+    cq, ck = _dev_i32(cu_q), _dev_i32(cu_k)
+    with torch.cuda.graph(graph):
+        kvc.kvc_prefill_attention_varlen(qd, kd, vd, cq, ck, max(lens_q), max(lens_k), out=out, lse=lse)
+    for _ in range(3):
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(B):
+            rows = slice(int(cu_q[b]), int(cu_q[b + 1]))
+            if b not in again:
+                assert torch.equal(out[rows], clean[0][rows]) and torch.equal(lse[rows], clean[1][rows]), b
+                continue
+            before = slice(int(cu_q[b]), int(cu_q[b + 1]) - 20)  # the rows that do not see the key
+            assert torch.equal(out[before], clean[0][before]) and torch.equal(lse[before], clean[1][before]), b
+            behind = slice(int(cu_q[b + 1]) - 20, int(cu_q[b + 1]))
+            if b % 2 == 0:
+                assert torch.isposinf(out[behind].float()).all() and torch.equal(lse[behind], clean[1][behind])
+    hit = [b for b in again if b % 2]
+    sel_q = np.concatenate([np.arange(cu_q[b], cu_q[b + 1]) for b in hit])
+    sel_k = np.concatenate([np.arange(cu_k[b], cu_k[b + 1]) for b in hit])
+    w_out, w_lse, tol, tol_lse = ref.prefill_varlen(
+        q[sel_q], _np(kd)[sel_k], v[sel_k], np.cumsum([0] + [lens_q[b] for b in hit]),
+        np.cumsum([0] + [lens_k[b] for b in hit]), 1 / math.sqrt(d))
+    _close(_np(out)[sel_q], w_out, tol, "out")
+    _close(_np(lse)[sel_q], w_lse, tol_lse, "lse")
+
+
 def test_prefill_varlen_head_major_layout():
     """q, k, v stored [heads][n][d], seen as [n][heads][d]."""
     rng = np.random.default_rng(27)
