@@ -523,11 +523,13 @@ int evict_cluster(const Paged& c, int64_t max_len) {
 }
 int64_t evict_segment(int64_t max_len, int cs) { return ((max_len + cs - 1) / cs + 31) / 32 * 32; }
 
-// The workspace: counters first (their place depends on the cache alone).
+// The workspace: counters first.  One per sequence is used, but what follows
+// starts behind one per pair: that much is zero before and after every call on
+// a paged cache, so that one workspace can serve them all.
 bool carve_evict(const Paged& c, int64_t max_len, int64_t budget, WsCursor* w, EvArgs* a) {
   const size_t bg = (size_t)c.batch * c.Hkv;
   a->max_move = std::max<int64_t>(1, evict_max_move(max_len, budget));
-  a->tickets = w->take<uint32_t>((size_t)c.batch);
+  a->tickets = w->take<uint32_t>(bg);
   a->moves = w->take<int32_t>(bg);
   a->lists = w->take<int32_t>(bg * 2 * (size_t)a->max_move);
   a->cluster = evict_cluster(c, max_len);
