@@ -448,8 +448,9 @@ kvc_status kvc_paged_append_workspace_size(const kvc_paged_cache* c, size_t* byt
  * KV retention -- the per-head selected entries of a prompt, or every token].
  * Sequence b brings the packed tokens [cu_seqlens[b], cu_seqlens[b+1]), len_b
  * of them.  With idx NULL all are kept, entry r being token r; with idx
- * [B][Hkv][kk] (local positions, as kvc_select_topk_varlen writes them) KV
- * head g keeps the first min(kk, len_b) of its row.  For every kept entry r:
+ * [B][Hkv][kk] (local positions, as kvc_select_topk_varlen writes them; not
+ * NULL with kk = 0 either, which keeps none) KV head g keeps the first
+ * min(kk, len_b) of its row.  For every kept entry r:
  *     slot = seq_lens[b] + r;  k, v of the token are copied bit for bit
  *     pos[slot]     = next_pos[b] + local position of the token
  *     weights[slot] = scores[g*total + packed position], or 0 without scores

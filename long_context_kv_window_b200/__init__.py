@@ -789,7 +789,7 @@ def kvc_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seq
     """Write tokens k, v [total][Hkv][d] behind the cache's entries: one per
     sequence, or the packed ones of cu_seqlens int32 [B+1] (max_seqlen bounds
     them); with idx int32 [B][Hkv][kk] (kvc_select_topk_varlen's) only the
-    selected ones of each KV head.  scores fp32 [Hkv][total] are the entries'
+    selected ones of each KV head (kk = 0: none).  scores fp32 [Hkv][total] are the entries'
     first weights.  Lengths and positions move on, on the device."""
     dev = cache.device
     if v is None:
@@ -816,12 +816,15 @@ def kvc_paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seq
     if scores is not None:
         _dense(scores, "scores", (Hkv, total), torch.float32, dev)
     _err_word(dev_err, dev)
+    # a selection of no entry has no address, and NULL means every token: any
+    # address says that there is a selection, of which nothing is read
+    sel = None if idx is None else idx.data_ptr() if kk else cu_seqlens.data_ptr()
     st = _raw_stream(stream, dev)
     sn, sh, _ = k.stride()
     with cache._lock:
         at, nbytes = cache._workspace(ws, "kvc_paged_append", (), st, stream)
         _check(_call(dev, lib().kvc_paged_append, cache._ref, k.data_ptr(), v.data_ptr(), sn if total > 1 else Hkv * d,
-                     sh if Hkv > 1 else d, _adr(cu_seqlens), total, int(max_seqlen), _adr(idx), kk, _adr(scores), at,
+                     sh if Hkv > 1 else d, _adr(cu_seqlens), total, int(max_seqlen), sel, kk, _adr(scores), at,
                      nbytes, _adr(dev_err), st), "kvc_paged_append")
     return cache
 

@@ -46,3 +46,18 @@ def test_one_workspace_serves_append_decode_and_evict_in_turn():
         ref.evict(t.pool, budget, 10)
         t.check_state("evict")
         assert not counters.any(), "evict"
+
+
+def test_append_of_an_empty_selection():
+    """A selection of no entry keeps none: the tokens are seen, nothing is written."""
+    rng = np.random.default_rng(5)
+    t = Paged(rng, [7, 0, 20], 2, 64, 16, room=40)
+    held = [x.clone() for x in (t.cache.k, t.cache.v, t.cache.weights, t.cache.pos)]
+    lens = [5, 0, 12]
+    _, kd = _bf16(rng, sum(lens), 2, 64)
+    kvc.kvc_paged_append(t.cache, kd, kd, _dev_i32(_cu(lens)), 12, idx=_dev_i32(np.zeros((3, 2, 0))), dev_err=t.err,
+                         scores=torch.ones((2, sum(lens)), device="cuda"))
+    t.pool.next_pos += np.array(lens, np.int32)
+    t.check_state()
+    for x, y in zip(held, (t.cache.k, t.cache.v, t.cache.weights, t.cache.pos)):
+        assert torch.equal(x, y)
