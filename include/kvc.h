@@ -508,7 +508,8 @@ kvc_status kvc_paged_decode_workspace_size(const kvc_paged_cache* c, int32_t num
  *           time per workspace
  *  dev_err  KVC_DEV_ERR_PAGES: a page id outside the pool or a length
  *           outside [0, max_len] (that sequence: out = 0, lse = -inf, weights
- *           unchanged); KVC_DEV_ERR_TIMEOUT
+ *           unchanged); KVC_DEV_ERR_TIMEOUT (the same for every KV head of a
+ *           sequence some of whose entries did not arrive)
  * At most 16 query heads per KV head.  Pages may be shared by sequences
  * unless `accumulate` is set (which also wants the weights 16-byte aligned).
  * fp32 accumulation from the bf16 values and the

@@ -78,7 +78,7 @@ struct PdArgs {
   float* z;       // [B][H]: log-sum-exp in log2 units (accumulate; else nullptr)
   float* logits;  // [B][H][ld], log2 units (accumulate)
   uint32_t* tickets;  // [B*Hkv]: runs of the pair done
-  float* part_ml;     // [2 * runs][G][2]: max, sum (sum -1: a page id was outside the pool)
+  float* part_ml;     // [2 * runs][G][2]: max, sum (sum -1: the piece has no result)
   float* part_o;      // [2 * runs][G][d]
   int32_t* err;
 };
@@ -312,6 +312,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   const int k_row = lane & 7, k_piece = lane >> 3;
   const int v_row = lane & 15, v_piece = lane >> 4;
   unsigned taken = 0;
+  bool lost = false;  // a wait of this warp gave up: from then on its stages are not the units it is at
   for (int64_t x = x0; x < x1;) {
     const Piece p = piece_at(x);
     x = p.next;
@@ -332,15 +333,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-    bool bad = false;
+    int marks = 0;  // why the piece has no result; 1: a page id outside the pool, 2: a unit that did not land
     for (int t = p.t0; t < p.t1; ++t) {
       const int s0 = t * kPdTile + warp * kPdUnit;  // first entry of the unit
       if (s0 >= p.len) break;
       const int st = (int)(taken % L::kStages);
-      if (!tc::mbar_wait(&bar[st], (taken / L::kStages) & 1, abort_flag)) break;
-      __syncwarp();
+      // the warp goes on or gives up as one
+      lost = lost || !__all_sync(0xffffffffu, tc::mbar_wait(&bar[st], (taken / L::kStages) & 1, abort_flag));
+      if (lost) {
+        marks |= 2;
+        break;
+      }
       const uint32_t kt = ring_u32 + (uint32_t)(st * L::kStage), vt = kt + L::kMat;
-      bad |= (bad_units >> st) & 1;
+      marks |= (bad_units >> st) & 1;
       const int left = p.len - s0;  // valid entries of the unit, if below 16
       if (left < kPdUnit) {  // what lies behind the entries must not meet p = 0 as infinity or NaN
         for (int i = lane; i < (kPdUnit - left) * (D / 8); i += 32) {
@@ -479,7 +484,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         r[D + 1] = l[hf];
       }
     }
-    if (lane == 0) flags[6 + warp] = bad;
+    if (lane == 0) flags[6 + warp] = marks;
     __syncthreads();
     const bool whole = p.t0 == 0 && p.t1 == p.nu;
     const int64_t h0 = (int64_t)p.b * a.H + p.g * G;  // first head of the pair
@@ -545,9 +550,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       }
       __syncthreads();
     };
-    bad = flags[6] | flags[7] | flags[8] | flags[9];
-    if (bad && tid == 0) set_dev_err(a.err, KVC_DEV_ERR_PAGES);
-    combine(whole ? -1 : 2 * run + (p.t0 == 0 ? 1 : 0), bad);
+    marks = flags[6] | flags[7] | flags[8] | flags[9];
+    if ((marks & 1) && tid == 0) set_dev_err(a.err, KVC_DEV_ERR_PAGES);
+    combine(whole ? -1 : 2 * run + (p.t0 == 0 ? 1 : 0), marks != 0);
     if (whole) continue;
     // ---- the last run of the pair joins the pieces
     const int c0 = rs.of(p.pair), c1 = rs.of(p.pair + p.nu - 1);
@@ -699,7 +704,7 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtasPerSm) paged_weights_kernel
     for (int h = 0; h < a.G; ++h) {
       const float z = a.z[h0 + h];
       const float4 y = *reinterpret_cast<const float4*>(a.logits + (h0 + h) * a.ld + s);
-      read &= z != -INFINITY;  // otherwise the sequence's pages could not be read
+      read &= z != -INFINITY;  // otherwise the pair's entries could not be read, or not all of them
       w[0] += tc::ex2_approx(y.x - z);
       w[1] += tc::ex2_approx(y.y - z);
       w[2] += tc::ex2_approx(y.z - z);

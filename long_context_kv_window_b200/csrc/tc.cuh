@@ -54,16 +54,30 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 #define KVC_WAIT_LIMIT_NS 2000000000ull
 #endif
 constexpr uint64_t kWaitLimitNs = KVC_WAIT_LIMIT_NS;
+// One probe of a bounded wait.  try_wait may suspend the thread for a while
+// that the hardware chooses, longer than the test build's bound.
+__device__ __forceinline__ bool mbar_probe(uint64_t* bar, uint32_t parity) {
+  if (kWaitLimitNs >= 1000) return mbar_try_wait(bar, parity);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 constexpr uint64_t kDrainLimitNs = 2000000000ull;  // 2 s
 constexpr uint32_t kWaitLimitIters = 1u << 28;
 
 // Wait for phase `parity` of `bar`.  Returns false (and raises *abort) when
 // the bound is hit or another role already aborted.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_probe(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 0; it < kWaitLimitIters; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_probe(bar, parity)) return true;
     if (*abort) return false;
     if ((it & 63) == 0 && global_timer_ns() - t0 > kWaitLimitNs) break;
   }

@@ -61,3 +61,52 @@ def test_append_of_an_empty_selection():
     t.check_state()
     for x, y in zip(held, (t.cache.k, t.cache.v, t.cache.weights, t.cache.pos)):
         assert torch.equal(x, y)
+
+
+def test_a_wait_that_gives_up_leaves_the_weights_alone():
+    """Accumulating decode with a wait bound of a nanosecond: a KV head some of
+    whose entries did not arrive in time has no result and leaves its weights as
+    they were; the others, if any, are the regular call's, to the last bit."""
+    import ctypes
+
+    from long_context_kv_window_b200 import build as kbuild
+
+    L = ctypes.CDLL(kbuild.SHORTWAIT_LIB)
+    fn = L.kvc_paged_decode_attention
+    fn.argtypes, fn.restype = kvc._SIGS["kvc_paged_decode_attention"]
+    B, Hkv, H, d, page, n = 6, 4, 8, 128, 16, 20000
+    pages = B * n // page
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn((pages, Hkv, page, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32).view(B, -1)
+    lens = _dev_i32([n - 7 * b for b in range(B)])
+    w0 = torch.rand((pages, Hkv, page), generator=g, device="cuda")
+    q = torch.randn((B, H, d), generator=g, device="cuda").bfloat16()
+    regular, short = (kvc.PagedCache(k, v, table, lens, weights=w0.clone()) for _ in range(2))
+    out, lse = kvc.kvc_paged_decode_attention(q, regular, scale=0.1, accumulate=True)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    got, got_lse, err = torch.empty_like(out), torch.empty_like(lse), torch.zeros(1, dtype=torch.int32, device="cuda")
+    seen = 0
+    for _ in range(20):
+        short.weights.copy_(w0)
+        err.zero_()
+        rc = fn(short._ref, q.data_ptr(), H * d, d, H, 0.1, short.capacity, 1, got.data_ptr(), got_lse.data_ptr(),
+                ws.data_ptr(), ws.numel(), err.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert rc == kvc.KVC_OK and err.item() in (0, kvc.KVC_DEV_ERR_TIMEOUT)
+        assert not ws[:4 * B * Hkv].any()
+        none = (got_lse == -math.inf).view(B, Hkv, H // Hkv)
+        assert (none.all(2) == none.any(2)).all() and none.any() == (err.item() != 0)
+        none = none.all(2)
+        rows = none.repeat_interleave(H // Hkv, 1)
+        assert (got[rows] == 0).all() and torch.equal(got[~rows], out[~rows]) and torch.equal(got_lse[~rows], lse[~rows])
+        kept = none[torch.arange(B, device="cuda").repeat_interleave(n // page)]  # [B * pages of a sequence][Hkv]
+        by_page = torch.empty_like(kept)
+        by_page[table.reshape(-1).long()] = kept
+        assert torch.equal(short.weights, torch.where(by_page[:, :, None], w0, regular.weights))
+        seen += err.item() != 0
+        if seen == 3:
+            break
+    assert seen, "no wait gave up"
+    kvc.kvc_paged_decode_attention(q, short, scale=0.1, out=got, lse=got_lse, ws=ws)
+    assert torch.equal(got, out) and torch.equal(got_lse, lse)
