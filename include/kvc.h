@@ -494,7 +494,9 @@ kvc_status kvc_paged_decode_workspace_size(const kvc_paged_cache* c, int32_t num
  * to the entry's weight  [StructKV 2.A: accumulated attention as a token's
  * centrality]:
  *     weights[j] += sum_{h in g} exp(s_j - lse[b, h])       (heads in order)
- * An empty sequence has out = 0 and lse = -inf.  What the pages hold past the
+ * An empty sequence has out = 0 and lse = -inf.  Where every s_j of a head is
+ * -inf the formulas have no value: its lse is -inf, its out and the weights of
+ * its KV head's entries become NaN.  What the pages hold past the
  * entries is not used, whatever it is (infinities and NaN included).
  *  q        [B][H][d] bf16, element (b, h, c) at q[b*q_stride_b + h*q_stride_h + c];
  *           16-byte aligned, strides multiples of 8

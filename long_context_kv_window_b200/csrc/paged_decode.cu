@@ -75,7 +75,7 @@ struct PdArgs {
   int64_t max_len, ld;  // ld: max_len rounded up to whole units
   float* out;     // [B][H][d]
   float* lse;     // [B][H] or nullptr
-  float* z;       // [B][H]: log-sum-exp in log2 units (accumulate; else nullptr)
+  float* z;       // [B][H]: log-sum-exp in log2 units, +inf (which none is): no result (accumulate; else nullptr)
   float* logits;  // [B][H][ld], log2 units (accumulate)
   uint32_t* tickets;  // [B*Hkv]: runs of the pair done
   float* part_ml;     // [2 * runs][G][2]: max, sum (sum -1: the piece has no result)
@@ -526,7 +526,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         if (c4 == 0) {
           const float z = none ? -INFINITY : M + log2f(Ls);
           if (a.lse) a.lse[h0 + h] = (float)((double)z * kLn2);
-          if (a.z) a.z[h0 + h] = z;
+          if (a.z) a.z[h0 + h] = none ? INFINITY : z;
         }
       }
       if (slot >= 0 || !__syncthreads_or(odd)) return;
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtasPerSm) paged_weights_kernel
     for (int h = 0; h < a.G; ++h) {
       const float z = a.z[h0 + h];
       const float4 y = *reinterpret_cast<const float4*>(a.logits + (h0 + h) * a.ld + s);
-      read &= z != -INFINITY;  // otherwise the pair's entries could not be read, or not all of them
+      read &= z != INFINITY;  // otherwise the pair's entries could not be read, or not all of them
       w[0] += tc::ex2_approx(y.x - z);
       w[1] += tc::ex2_approx(y.y - z);
       w[2] += tc::ex2_approx(y.z - z);

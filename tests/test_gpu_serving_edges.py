@@ -110,3 +110,27 @@ def test_a_wait_that_gives_up_leaves_the_weights_alone():
     assert seen, "no wait gave up"
     kvc.kvc_paged_decode_attention(q, short, scale=0.1, out=got, lse=got_lse, ws=ws)
     assert torch.equal(got, out) and torch.equal(got_lse, lse)
+
+
+@pytest.mark.parametrize("lens", [[50, 33], [3000, 700]])
+def test_decode_over_entries_whose_logits_are_all_minus_infinity(lens):
+    """exp(s - lse) of such a head is NaN, and so is what the entries' weights
+    become: the head is not taken for one whose pages could not be read."""
+    rng = np.random.default_rng(11)
+    t = Paged(rng, lens, 2, 64, 16)
+    q, qd = _bf16(rng, 2, 6, 64)
+    qd[:, :, 9] = qd[:, :, 9].abs() + 1
+    clean = [x.clone() for x in kvc.kvc_paged_decode_attention(qd, t.cache)]
+    before = t.cache.weights.clone()
+    at = [x.tolist() if isinstance(x, np.ndarray) else x for x in t.pool.at(0, 1, np.arange(lens[0]))]
+    t.cache.k[at[0], 1, at[2], 9] = -math.inf
+    out, lse = kvc.kvc_paged_decode_attention(qd, t.cache, accumulate=True, dev_err=t.err)
+    torch.cuda.synchronize()
+    assert t.err.item() == 0
+    assert out[0, 3:].isnan().all() and (lse[0, 3:] == -math.inf).all()
+    assert torch.equal(out[0, :3], clean[0][0, :3]) and torch.equal(out[1], clean[0][1])
+    assert torch.equal(lse[0, :3], clean[1][0, :3]) and torch.equal(lse[1], clean[1][1])
+    assert t.cache.weights[at[0], 1, at[2]].isnan().all()
+    others = torch.ones_like(before, dtype=torch.bool)
+    others[at[0], 1, at[2]] = False
+    assert t.cache.weights[others].isfinite().all() and not torch.equal(t.cache.weights[others], before[others])
