@@ -370,7 +370,8 @@ kvc_status kvc_prefill_varlen_workspace_size(int32_t num_heads, int32_t num_kv_h
  *     s_ij     = scale * q[i, h, :] . k[j, g, :],   g = h / G
  *     lse[i,h] = ln sum_{j <= i + lk - lq} exp(s_ij)
  *     out[i,h] = sum_{j <= i + lk - lq} exp(s_ij - lse[i,h]) v[j, g, :]
- * A query that sees no key (lq > lk) has out = 0 and lse = -inf.  Keys and
+ * A query that sees no key (lq > lk) has out = 0 and lse = -inf; where every
+ * s_ij it sees is -inf the formulas have no value: lse = -inf, out = NaN.  Keys and
  * values a query does not see (later positions, other sequences) do not enter
  * its row, whatever they hold: infinities and NaN there change nothing.
  *  q     [total_q][H][d] bf16, element (i, h, c) at q[i*q_stride_n + h*q_stride_h + c]

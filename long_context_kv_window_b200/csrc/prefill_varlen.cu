@@ -807,13 +807,15 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const VarArg
   const int64_t n = a.total_q * a.H;
   if (rh >= n) return;
   const int row = (int)(rh / a.H);
-  bool owned = false;
+  int keys = -1;  // the keys that the row sees; -1: a row of no (sound) sequence
   for (int b = lane; b < a.batch; b += 32) {
     bool bad;
     seq_blocks(a, b, &bad);
-    owned |= !bad && row >= a.cu_q[b] && row < a.cu_q[b + 1];
+    if (bad || row < a.cu_q[b] || row >= a.cu_q[b + 1]) continue;
+    keys = std::max(0, row + 1 - a.cu_q[b + 1] + (a.cu_k[b + 1] - a.cu_k[b]));
   }
-  if (!__any_sync(0xffffffffu, owned)) return;
+  keys = __reduce_max_sync(0xffffffffu, keys);
+  if (keys < 0) return;
   float Z = -INFINITY;
   for (int s = 0; s < a.splits; ++s) Z = fmaxf(Z, a.part_z[s * n + rh]);
   float acc[D / 32], sum = 0.f;
@@ -822,14 +824,14 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const VarArg
 #pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
     const float z = a.part_z[s * n + rh];
-    if (z == -INFINITY) continue;  // no key of the split
+    if (z == -INFINITY) continue;  // no key of the split, or all its logits are -inf
     const float w = tc::ex2_approx(z - Z);
     sum += w;
     const float* o = a.part_o + (s * n + rh) * D + lane * (D / 32);
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] += w * o[e];
   }
-  const bool seen = Z != -INFINITY;
+  const bool seen = keys > 0;  // not told by Z: it is -inf as well where every logit is, or is NaN
   const float inv = seen ? 1.f / sum : 0.f;
   if (a.out) {
 #pragma unroll

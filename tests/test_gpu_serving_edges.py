@@ -134,3 +134,35 @@ def test_decode_over_entries_whose_logits_are_all_minus_infinity(lens):
     others = torch.ones_like(before, dtype=torch.bool)
     others[at[0], 1, at[2]] = False
     assert t.cache.weights[others].isfinite().all() and not torch.equal(t.cache.weights[others], before[others])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_varlen_rows_without_a_finite_logit_split_or_not(d):
+    """A row that sees keys, all at -inf, has the log-sum-exp -inf and NaN as
+    output; a NaN in its query makes NaN of both.  That does not depend on how
+    many CTAs share its keys, and rows that see no key stay 0 and -inf."""
+    rng = np.random.default_rng(d)
+    H, Hkv, lq, lk = 4, 2, 24, 2600
+    _, q = _bf16(rng, lq, H, d)
+    _, k = _bf16(rng, lk, Hkv, d)
+    _, v = _bf16(rng, lk, Hkv, d)
+    q[:, :, 3] = q[:, :, 3].abs() + 1
+    k[:, 1, 3] = -math.inf  # the second KV head's logits
+    q[5, 0, 7] = math.nan
+    none = torch.empty((0, Hkv, d), dtype=torch.bfloat16, device="cuda")
+    assert kvc.prefill_varlen_workspace_size(H, Hkv, d, 2, 2 * lq, lq, lk) > 0  # split
+    many = 90
+    assert kvc.prefill_varlen_workspace_size(H, Hkv, d, many, many * lq, lq, lk) == 0
+    for B in (2, many):  # the last sequence has no key
+        lens_k = [lk] * (B - 1) + [0]
+        out, lse = (x.clone() for x in kvc.kvc_prefill_attention_varlen(
+            q.repeat(B, 1, 1), torch.cat([k] * (B - 1) + [none]), torch.cat([v] * (B - 1) + [none]),
+            _dev_i32(_cu([lq] * B)), _dev_i32(_cu(lens_k)), lq, lk))
+        for b in range(B - 1):
+            o, z = out[b * lq:(b + 1) * lq], lse[b * lq:(b + 1) * lq]
+            assert o[:, 2:].isnan().all() and (z[:, 2:] == -math.inf).all(), (B, b)
+            assert o[5, 0].isnan().all() and z[5, 0].isnan(), (B, b)
+            rest = torch.ones((lq, 2), dtype=torch.bool, device="cuda")
+            rest[5, 0] = False
+            assert o[:, :2][rest].isfinite().all() and z[:, :2][rest].isfinite().all(), (B, b)
+        assert (out[-lq:] == 0).all() and (lse[-lq:] == -math.inf).all()
