@@ -93,12 +93,17 @@ struct VarArgs {
   int nt;                // tokens per tile: 128 / G
   float c;               // scale * log2(e)
   int splits;            // CTAs that share the keys of a block
-  float* part_z;         // splits > 1: [splits][total_q][H] log-sum-exp of the split, log2 units
-  float* part_o;         // splits > 1: [splits][total_q][H][D] its output
+  int64_t part_rows;     // splits > 1: rows of the partial results, min(total_q, batch * max_q)
+  float* part_z;         // [splits][part_rows][H] log-sum-exp of the split, log2 units
+  float* part_o;         // [splits][part_rows][H][D] its output
   uint16_t* out;         // [total_q][H][D] or nullptr
   float* lse;            // [total_q][H] or nullptr
   int32_t* err;
 };
+
+// The partial results hold the rows of q as they lie there, or, where q has
+// room for many more rows than the sequences can have, max_q rows for each.
+__device__ __forceinline__ bool parts_by_sequence(const VarArgs& a) { return a.part_rows < a.total_q; }
 
 constexpr int kVBarBytes = 2048;
 
@@ -690,6 +695,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       const int q0 = b->q0, k0 = b->k0, i0 = b->i0, g = b->g, h = g * a.G + r % a.G;
       const bool own = mine();
       const int64_t row = (int64_t)(q0 + i0) + ti;  // the row of out and lse
+      const int64_t part = b->split * a.part_rows + (parts_by_sequence(a) ? b->seq * a.max_q + i0 + ti : row);
       const float sum_row = both((float)l, [](float x0, float x1) { return x0 + x1; });
       {
         tc::tc_fence_after();
@@ -727,7 +733,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
               }
             }
           if (a.part_o) {
-            float4* po = reinterpret_cast<float4*>(a.part_o + (((int64_t)b->split * a.total_q + row) * a.H + h) * D + col);
+            float4* po = reinterpret_cast<float4*>(a.part_o + (part * a.H + h) * D + col);
             if (own)
 #pragma unroll
               for (int u = 0; u < 8; ++u) po[u] = make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
@@ -765,7 +771,7 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           const float f2 = frexpf(sum_row, &e2);
           const double z = (double)m_ref + ((double)e2 + (double)log2f(f2));
           if (a.part_z)
-            a.part_z[((int64_t)b->split * a.total_q + row) * a.H + h] = seen ? (float)z : -INFINITY;
+            a.part_z[part * a.H + h] = seen ? (float)z : -INFINITY;
           else if (a.lse)
             a.lse[row * a.H + h] = seen ? (float)(z * kLn2) : -INFINITY;
         }
@@ -796,38 +802,47 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   }
 }
 
-// Joins the splits of a row, one warp per (query, head):
+// Joins the splits of a row, one warp per (row of the partial results, head):
 // out = sum_s 2^(z_s - Z) o_s, Z = log2 sum_s 2^z_s; rows of no (sound) sequence are left as they are.
 constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const VarArgs a) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t rh = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);  // row * H + head
-  const int64_t n = a.total_q * a.H;
-  if (rh >= n) return;
-  const int row = (int)(rh / a.H);
-  int keys = -1;  // the keys that the row sees; -1: a row of no (sound) sequence
-  for (int b = lane; b < a.batch; b += 32) {
+  const int ph = (int)blockIdx.x * (kJoinThreads / 32) + (int)(threadIdx.x >> 5);  // partial row * H + head
+  const int n = (int)a.part_rows * a.H;  // times the splits below 2^17
+  if (ph >= n) return;
+  const int part = ph / a.H;
+  int row = part;  // of q
+  int keys = -1;       // the keys that the row sees; -1: a row of no (sound) sequence
+  auto look = [&](int b) {
     bool bad;
     seq_blocks(a, b, &bad);
-    if (bad || row < a.cu_q[b] || row >= a.cu_q[b + 1]) continue;
+    if (bad || row < a.cu_q[b] || row >= a.cu_q[b + 1]) return;
     keys = std::max(0, row + 1 - a.cu_q[b + 1] + (a.cu_k[b + 1] - a.cu_k[b]));
+  };
+  if (parts_by_sequence(a)) {
+    const int most = (int)a.max_q, b = part / most;
+    row = a.cu_q[b] + part % most;
+    look(b);
+  } else {
+    for (int b = lane; b < a.batch; b += 32) look(b);
   }
   keys = __reduce_max_sync(0xffffffffu, keys);
   if (keys < 0) return;
+  const int64_t rh = (int64_t)row * a.H + ph % a.H;  // of out and lse
   float Z = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) Z = fmaxf(Z, a.part_z[s * n + rh]);
+  for (int s = 0; s < a.splits; ++s) Z = fmaxf(Z, a.part_z[s * n + ph]);
   float acc[D / 32], sum = 0.f;
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < a.splits; ++s) {
-    const float z = a.part_z[s * n + rh];
+    const float z = a.part_z[s * n + ph];
     if (z == -INFINITY) continue;  // no key of the split, or all its logits are -inf
     const float w = tc::ex2_approx(z - Z);
     sum += w;
-    const float* o = a.part_o + (s * n + rh) * D + lane * (D / 32);
+    const float* o = a.part_o + (s * n + ph) * D + lane * (D / 32);
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] += w * o[e];
   }
@@ -897,7 +912,7 @@ kvc_status launch_varlen(dim3 grid, cudaStream_t st, const CUtensorMap (&maps)[3
   KVC_CUDA_TRY(l.run(prefill_varlen_kernel<D>, maps[0], maps[1], maps[2], a));
   count_launch();
   if (a.splits == 1) return KVC_OK;
-  const int64_t warps = a.total_q * a.H, per = kJoinThreads / 32;
+  const int64_t warps = a.part_rows * a.H, per = kJoinThreads / 32;
   const Launch j(dim3((unsigned)((warps + per - 1) / per)), dim3(kJoinThreads), 0, st);
   KVC_CUDA_TRY(j.run(prefill_join_kernel<D>, a));
   count_launch();
@@ -914,7 +929,8 @@ int64_t varlen_blocks(int nt, int batch, int64_t total_q, int64_t max_q) {
 // or a small chunk's queries) leave most SMs without a CTA; the splits are
 // chosen by the time of all waves, in key tiles, with kSplitCost for what a CTA
 // and the joining cost beside its tiles.  At most three CTAs per SM come of it,
-// which bounds the workspace.
+// which bounds the workspace: their blocks hold at most 256 (row, head) pairs
+// each, whatever room q has behind the sequences.
 constexpr int64_t kSplitCost = 6;
 int varlen_splits(int64_t items, int64_t max_k) {
   const int64_t sms = num_sms(), tiles = (max_k + kVT - 1) / kVT;
@@ -930,7 +946,8 @@ int varlen_splits(int64_t items, int64_t max_k) {
 bool carve_varlen(int H, int Hkv, int d, int batch, int64_t total_q, int64_t max_q, int64_t max_k, WsCursor* w, VarArgs* a) {
   a->splits = varlen_splits(varlen_blocks(kVT / (H / Hkv), batch, total_q, max_q) * Hkv, max_k);
   if (a->splits == 1) return true;
-  const size_t rows = (size_t)a->splits * (size_t)total_q * H;
+  a->part_rows = std::min(total_q, batch * max_q);
+  const size_t rows = (size_t)a->splits * (size_t)a->part_rows * H;
   a->part_z = w->take<float>(rows);
   a->part_o = w->take<float>(rows * d);
   return w->ok;

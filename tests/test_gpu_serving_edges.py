@@ -166,3 +166,34 @@ def test_prefill_varlen_rows_without_a_finite_logit_split_or_not(d):
             rest[5, 0] = False
             assert o[:, :2][rest].isfinite().all() and z[:, :2][rest].isfinite().all(), (B, b)
         assert (out[-lq:] == 0).all() and (lse[-lq:] == -math.inf).all()
+
+
+@pytest.mark.parametrize("lq,most,H,d", [([20], 20, 8, 128), ([20, 0, 13], 20, 8, 64), ([3, 40, 17], 64, 4, 128)])
+def test_prefill_varlen_split_rows_in_a_padded_batch(lq, most, H, d):
+    """Few rows over many keys in a q with room for thousands: as in a tight
+    one, and the room behind is left as it was."""
+    rng = np.random.default_rng(sum(lq) + H)
+    Hkv, lk = 2, [2900 - 150 * b for b in range(len(lq))]
+    room = 5000
+    q, qd = _bf16(rng, sum(lq), H, d)
+    k, kd = _bf16(rng, sum(lk), Hkv, d)
+    v, vd = _bf16(rng, sum(lk), Hkv, d)
+    big = torch.full((room, H, d), math.nan, dtype=torch.bfloat16, device="cuda")
+    big[:sum(lq)] = qd
+    got = []
+    for x in (qd, big):
+        out = torch.full(x.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full(x.shape[:2], 7.0, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        assert kvc.prefill_varlen_workspace_size(H, Hkv, d, len(lq), x.shape[0], most, max(lk)) > 0
+        kvc.kvc_prefill_attention_varlen(x, kd, vd, _dev_i32(_cu(lq)), _dev_i32(_cu(lk)), most, max(lk), out=out, lse=lse,
+                                         dev_err=err)
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        got.append((out, lse))
+    w_out, w_lse, tol, tol_lse = ref.prefill_varlen(q, k, v, _cu(lq), _cu(lk), 1 / math.sqrt(d))
+    n = sum(lq)
+    for out, lse in got:
+        _close(_np(out)[:n], w_out, tol, "out")
+        _close(_np(lse)[:n], w_lse, tol_lse, "lse")
+        assert (out[n:] == 7).all() and (lse[n:] == 7).all()

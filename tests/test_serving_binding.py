@@ -25,3 +25,17 @@ def test_a_selection_of_no_entry_is_not_every_token(calls):
         kvc.kvc_paged_append(c, p, p, cu, 5, idx=idx)
         sel, kk = calls[-1][8:10]
         assert (sel is None) == null and sel != 0 and kk == (0 if idx is None else idx.shape[2])
+
+
+def test_prefill_workspace_does_not_grow_with_room_behind_the_sequences():
+    """A few rows over many keys in a q with room for many more rows."""
+    from long_context_kv_window_b200 import build
+    build.build()
+    size = kvc.prefill_varlen_workspace_size
+    tight = size(32, 8, 128, 3, 60, 20, 30000)
+    assert tight > 0
+    assert size(32, 8, 128, 3, 1 << 20, 20, 30000) == tight
+    # at most three CTAs per SM (148 of them) with 256 rows each, of d + 1 floats
+    for H, Hkv, d, B, tq, mq, mk in ((32, 8, 128, 1, 1 << 30, 32, 1 << 17), (8, 1, 64, 5, 1 << 20, 100, 1 << 20),
+                                     (1, 1, 128, 200, 300, 101, 1 << 20), (40, 8, 128, 4, 7, 7, 1 << 15)):
+        assert size(H, Hkv, d, B, tq, mq, mk) <= 3 * 148 * 256 * (d + 1) * 4 + 512
