@@ -588,11 +588,20 @@ def kvc_prefill_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, sca
 
 
 @functools.lru_cache(maxsize=256)
-def prefill_varlen_workspace_size(H: int, Hkv: int, d: int, batch: int, total_q: int, max_q: int, max_k: int) -> int:
+def _prefill_varlen_bytes(index: Optional[int], *shape: int) -> int:
     out = ctypes.c_size_t(0)
-    _check(lib().kvc_prefill_varlen_workspace_size(H, Hkv, d, batch, total_q, max_q, max_k, ctypes.byref(out)),
-           "kvc_prefill_varlen_workspace_size")
+    fn = lib().kvc_prefill_varlen_workspace_size
+    _check(fn(*shape, ctypes.byref(out)) if index is None else
+           _call(torch.device("cuda", index), fn, *shape, ctypes.byref(out)), "kvc_prefill_varlen_workspace_size")
     return int(out.value)
+
+
+def prefill_varlen_workspace_size(H: int, Hkv: int, d: int, batch: int, total_q: int, max_q: int, max_k: int,
+                                  dev: Optional[torch.device] = None) -> int:
+    """Workspace bytes of a call with these sizes on `dev`, whose number of SMs
+    they depend on (default: the current device)."""
+    index = dev.index if dev is not None else torch.cuda.current_device() if torch.cuda.is_available() else None
+    return _prefill_varlen_bytes(index, H, Hkv, d, batch, total_q, max_q, max_k)
 
 
 def _adr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -666,7 +675,7 @@ def kvc_prefill_attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     _dense(lse, "lse", (total_q, H), torch.float32, dev)
     _err_word(dev_err, dev)
     if ws is None:
-        need = prefill_varlen_workspace_size(H, Hkv, d, B, total_q, max_seqlen_q, max_seqlen_k)
+        need = prefill_varlen_workspace_size(H, Hkv, d, B, total_q, int(max_seqlen_q), int(max_seqlen_k), dev)
         ws = _scratch(need, dev, stream) if need else None
     sc = float(1.0 / math.sqrt(d) if scale is None else scale)
     _check(_call(dev, lib().kvc_prefill_attention_varlen, _adr(q), _stride(q, 0), _stride(q, 1), _adr(k),

@@ -39,3 +39,30 @@ def test_prefill_workspace_does_not_grow_with_room_behind_the_sequences():
     for H, Hkv, d, B, tq, mq, mk in ((32, 8, 128, 1, 1 << 30, 32, 1 << 17), (8, 1, 64, 5, 1 << 20, 100, 1 << 20),
                                      (1, 1, 128, 200, 300, 101, 1 << 20), (40, 8, 128, 4, 7, 7, 1 << 15)):
         assert size(H, Hkv, d, B, tq, mq, mk) <= 3 * 148 * 256 * (d + 1) * 4 + 512
+
+
+def test_prefill_workspace_is_that_of_the_tensors_device(monkeypatch):
+    """The size hangs on the SMs of the device that the tensors are on, which
+    need not be the current one."""
+    current = [0]
+
+    def call(dev, fn, *args):
+        before, current[0] = current[0], dev.index
+        try:
+            return fn(*args)
+        finally:
+            current[0] = before
+
+    class Lib:
+        @staticmethod
+        def kvc_prefill_varlen_workspace_size(*args):
+            args[-1]._obj.value = 1000 + current[0]
+            return kvc.KVC_OK
+
+    monkeypatch.setattr(kvc, "_call", call)
+    monkeypatch.setattr(kvc, "lib", Lib)
+    shape = (6, 2, 64, 11, 977, 131, 8191)  # of no other test
+    for _ in range(2):
+        assert [kvc.prefill_varlen_workspace_size(*shape, torch.device("cuda", i)) for i in (0, 1, 0, 2)] == [
+            1000, 1001, 1000, 1002]
+    kvc._prefill_varlen_bytes.cache_clear()
