@@ -632,12 +632,22 @@ def _scratch(nbytes: int, dev: torch.device, stream: Optional[torch.cuda.Stream]
         return _workspace(nbytes, dev)
 
 
+def _result(shape, dtype: torch.dtype, dev: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A result for a call on `stream`: memory in that stream's order, so that
+    nothing that is still to run on the current stream uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _used_on(stream: Optional[torch.cuda.Stream], *made: Optional[torch.Tensor]) -> None:
-    """Tell the allocator that results made here are written on `stream`."""
+    """Tell the allocator that results made for `stream` are used on the
+    current stream, where the caller goes on with them."""
     if stream is not None:
         for t in made:
             if t is not None:
-                t.record_stream(stream)
+                t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def kvc_prefill_attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -667,11 +677,11 @@ def kvc_prefill_attention_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     _vector(cu_seqlens_k, "cu_seqlens_k", B + 1, torch.int32, dev)
     made_out = made_lse = None
     if out is None and want_out:
-        out = made_out = torch.empty((total_q, H, d), dtype=torch.bfloat16, device=dev)
+        out = made_out = _result((total_q, H, d), torch.bfloat16, dev, stream)
     if out is not None:
         _dense(out, "out", (total_q, H, d), _BF16_BITS, dev)
     if lse is None:
-        lse = made_lse = torch.empty((total_q, H), dtype=torch.float32, device=dev)
+        lse = made_lse = _result((total_q, H), torch.float32, dev, stream)
     _dense(lse, "lse", (total_q, H), torch.float32, dev)
     _err_word(dev_err, dev)
     if ws is None:
@@ -857,10 +867,10 @@ def kvc_paged_decode_attention(q: torch.Tensor, cache: PagedCache, scale: Option
         raise ValueError("accumulate needs a cache with weights")
     made_out = made_lse = None
     if out is None:
-        out = made_out = torch.empty((B, H, d), dtype=torch.float32, device=dev)
+        out = made_out = _result((B, H, d), torch.float32, dev, stream)
     _dense(out, "out", (B, H, d), torch.float32, dev)
     if lse is None:
-        lse = made_lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+        lse = made_lse = _result((B, H), torch.float32, dev, stream)
     _dense(lse, "lse", (B, H), torch.float32, dev)
     _err_word(dev_err, dev)
     max_len = cache._max_len(max_len)

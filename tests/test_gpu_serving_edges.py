@@ -197,3 +197,47 @@ def test_prefill_varlen_split_rows_in_a_padded_batch(lq, most, H, d):
         _close(_np(out)[:n], w_out, tol, "out")
         _close(_np(lse)[:n], w_lse, tol_lse, "lse")
         assert (out[n:] == 7).all() and (lse[n:] == 7).all()
+
+
+@pytest.mark.parametrize("op", ["prefill", "decode"])
+def test_results_of_a_call_on_another_stream_have_memory_of_their_own(op):
+    """A tensor that was freed while work of the current stream still reads it is
+    not where a call on another stream, which does not wait for that work, puts
+    its results; nor is a result that the current stream still reads where the
+    next call puts its own."""
+    rng = np.random.default_rng(13)
+    s = torch.cuda.Stream()
+    if op == "prefill":
+        n, H, d, dtype = 2000, 8, 128, torch.bfloat16
+        _, q = _bf16(rng, n, H, d)
+        _, k = _bf16(rng, n, 2, d)
+        cu = _dev_i32([0, n])
+
+        def call(stream, q=q):
+            return kvc.kvc_prefill_attention_varlen(q, k, k, cu, cu, n, n, stream=stream)
+    else:
+        n, H, d, dtype = 256, 32, 128, torch.float32
+        t = Paged(rng, [20] * n, 2, d, 16)
+        _, q = _bf16(rng, n, H, d)
+
+        def call(stream, q=q):
+            return kvc.kvc_paged_decode_attention(q, t.cache, stream=stream)
+    other_q = -q
+    call(s)  # the cache's workspace of that stream
+    want = [x.clone() for x in call(None)]
+    held = torch.full((n, H, d), 3.0, dtype=dtype, device="cuda")
+    copy = torch.empty_like(held)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(300_000_000)
+    copy.copy_(held)
+    del held
+    out, lse = call(s)
+    torch.cuda.synchronize()
+    assert (copy == 3.0).all()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    torch.cuda._sleep(300_000_000)
+    copy.copy_(out)
+    del out
+    other = call(s, other_q)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want[0]) and not torch.equal(other, want[0])
