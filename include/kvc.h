@@ -502,7 +502,9 @@ kvc_status kvc_paged_decode_workspace_size(const kvc_paged_cache* c, int32_t num
  *  q        [B][H][d] bf16, element (b, h, c) at q[b*q_stride_b + h*q_stride_h + c];
  *           16-byte aligned, strides multiples of 8
  *  max_len  upper bound of seq_lens (host value), <= max_pages * page_size;
- *           batch * max_len below 2^36, batch * num_kv_heads * max_len below 2^40
+ *           the workspace of an accumulating call holds batch * num_heads *
+ *           max_len floats, and the grid goes by it, so a bound near the
+ *           longest sequence pays; batch * max_len below 2^36, batch * num_kv_heads * max_len below 2^40
  *  out      [B][H][d] fp32, contiguous, 16-byte aligned
  *  lse      [B][H] fp32 contiguous, or NULL
  *  ws       kvc_paged_decode_workspace_size(...) bytes, 256-B aligned,
@@ -542,7 +544,8 @@ kvc_status kvc_paged_evict_workspace_size(const kvc_paged_cache* c, int64_t max_
  * up.  Then seq_lens[b] = budget.  Attention does not depend on the order of
  * the entries, so nothing else has to move; slots >= budget keep what they
  * held, and sequences of at most `budget` entries are not touched.
- *  max_len  upper bound of seq_lens (host value), <= max_pages * page_size
+ *  max_len  upper bound of seq_lens (host value), <= max_pages * page_size;
+ *           the launches and the workspace go by max_len - budget
  *  budget   >= 1; recent in [0, budget]
  *  ws       kvc_paged_evict_workspace_size(...) bytes, 256-B aligned,
  *           the first batch * num_kv_heads * 4 bytes (at most) ZERO-FILLED

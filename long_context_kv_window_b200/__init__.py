@@ -715,7 +715,15 @@ class PagedCache:
     (the calls read them on the device), the tensors themselves stay.  Each
     call that is not given a workspace uses one the cache keeps for the stream
     it runs on; inside a stream capture it makes one for that graph alone, so
-    that graphs of one cache share none.
+    that graphs of one cache share none.  A workspace that the caller gives is
+    zero-filled before its first use and serves one call at a time.
+
+    max_len of a call, the block table's room where it is not given, is not
+    only checked: workspaces and launches go by it, whatever the sequences
+    hold.  An accumulating decode keeps batch * H * max_len floats per stream;
+    an eviction launches what max_len - budget entries too many would need (a
+    second kernel past 64), and past 48K entries per CTA keeps keys in memory.
+    So give a bound near the longest sequence where the room is far larger.
     """
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -780,7 +788,11 @@ class PagedCache:
             out = ctypes.c_size_t(0)
             _check(_call(self.device, getattr(lib(), call + "_workspace_size"), self._ref, *size_args,
                          ctypes.byref(out)), call + "_workspace_size")
-            need = self._need[call, size_args] = max(int(out.value), 1)
+            if len(self._need) >= 256:  # a bound that moves on with the lengths
+                self._need.clear()
+            # in eighths of a power of two: a bound that grows makes a larger workspace a few times per doubling only
+            step = 1 << max(8, int(out.value).bit_length() - 4)
+            need = self._need[call, size_args] = max(-(-int(out.value) // step), 1) * step
         if stream is None and torch.cuda.current_device() == self.device.index:
             capturing = torch.cuda.is_current_stream_capturing()
         else:  # the state of the stream the call runs on
@@ -856,7 +868,7 @@ def kvc_paged_decode_attention(q: torch.Tensor, cache: PagedCache, scale: Option
     """One decode query per head of every sequence, q [B][H][d], over the
     entries the cache holds; returns (out fp32 [B][H][d], lse fp32 [B][H]).
     max_len bounds the entries per sequence (default: the block table's
-    room).  accumulate adds every entry's attention to the cache's weights."""
+    room; PagedCache says what hangs on it).  accumulate adds every entry's attention to the cache's weights."""
     _bf16(q, "q", 3)
     dev = q.device
     _same_device(cache.device, q=q)
@@ -890,7 +902,8 @@ def kvc_paged_evict(cache: PagedCache, budget: int, recent: int, max_len: Option
                     stream=None) -> PagedCache:
     """Bring every sequence back to `budget` entries per KV head: the entries
     of the last `recent` positions and the largest weights are kept, in place
-    (kept entries above the budget move into the slots given up below it)."""
+    (kept entries above the budget move into the slots given up below it).
+    max_len as for kvc_paged_decode_attention."""
     dev = cache.device
     if cache.weights is None:
         raise ValueError("eviction ranks by the cache's weights: it has none")

@@ -241,3 +241,28 @@ def test_results_of_a_call_on_another_stream_have_memory_of_their_own(op):
     other = call(s, other_q)[0]
     torch.cuda.synchronize()
     assert torch.equal(copy, want[0]) and not torch.equal(other, want[0])
+
+
+def test_a_bound_that_follows_the_lengths_keeps_few_workspaces():
+    """max_len given exactly, a token longer each step: the kept workspace is made
+    anew a few times, and what the cache remembers of the sizes stays small."""
+    rng = np.random.default_rng(17)
+    t = Paged(rng, [300, 12], 2, 64, 16, room=1400)
+    _, k = _bf16(rng, 2, 2, 64)
+    _, q = _bf16(rng, 2, 4, 64)
+    made, n = set(), 300
+    for step in range(1400):
+        kvc.kvc_paged_append(t.cache, k, k, dev_err=t.err)
+        n += 1
+        kvc.kvc_paged_decode_attention(q, t.cache, max_len=n, accumulate=True, dev_err=t.err)
+        kvc.kvc_paged_evict(t.cache, 4000, 1, max_len=n, dev_err=t.err)
+        made |= {(key, kept[2]) for key, kept in t.cache._ws.items()}
+        assert len(t.cache._need) <= 256
+    assert len(made) < 30
+    t.pool.seq_lens += 1400
+    at = [t.pool.at(b, g, np.arange(m)) for b, m in enumerate(t.pool.seq_lens) for g in range(2)]
+    kd, vd = _np(t.cache.k), _np(t.cache.v)
+    for i in at:
+        t.pool.k[i], t.pool.v[i] = kd[i], vd[i]
+    t.pool.weights = t.cache.weights.cpu().numpy().copy()
+    t.decode(rng, 4, True, max_len=n)
