@@ -1010,8 +1010,8 @@ extern "C" kvc_status kvc_prefill_attention_varlen(
   a.out = out;
   a.lse = lse;
   a.err = dev_err;
-  const int64_t blocks = varlen_blocks(a.nt, batch, total_q, max_seqlen_q);
-  if (blocks == 0) return KVC_OK;
+  // with max_seqlen_q 0 there is no block, but a sequence that has queries all the same is to be reported
+  const int64_t blocks = std::max<int64_t>(1, varlen_blocks(a.nt, batch, total_q, max_seqlen_q));
   KVC_CHECK_ARG(blocks * num_kv_heads < (int64_t(1) << 31), "too many query blocks for one call");
   WsCursor w{static_cast<char*>(ws), ws_bytes};
   if (!carve_varlen(num_heads, num_kv_heads, head_dim, batch, total_q, max_seqlen_q, max_seqlen_k, &w, &a) ||

@@ -266,3 +266,15 @@ def test_a_bound_that_follows_the_lengths_keeps_few_workspaces():
         t.pool.k[i], t.pool.v[i] = kd[i], vd[i]
     t.pool.weights = t.cache.weights.cpu().numpy().copy()
     t.decode(rng, 4, True, max_len=n)
+
+
+def test_prefill_varlen_queries_where_the_bound_says_none():
+    """max_seqlen_q = 0: sequences without queries are fine, one with some is reported."""
+    q = torch.randn((6, 4, 64), device="cuda").bfloat16()
+    for cu, want in (([0, 0, 0], 0), ([0, 0, 6], kvc.KVC_DEV_ERR_SEQLENS)):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = torch.full_like(q, 7.0), torch.full((6, 4), 7.0, device="cuda")
+        kvc.kvc_prefill_attention_varlen(q, q[:, :2], q[:, :2], _dev_i32(cu), _dev_i32([0, 3, 6]), 0, 3, out=out, lse=lse,
+                                         dev_err=err)
+        torch.cuda.synchronize()
+        assert err.item() == want and (out == 7).all() and (lse == 7).all()
