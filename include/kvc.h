@@ -381,6 +381,7 @@ kvc_status kvc_prefill_varlen_workspace_size(int32_t num_heads, int32_t num_kv_h
  *        at most total_q / total_k; entries of out and lse past
  *        cu_seqlens_q[batch] are left as they were
  *  batch 1..1024
+ *  total_q  0: nothing is read or written
  *  max_seqlen_q, max_seqlen_k  upper bounds of lq and lk (host values)
  *  out   [total_q][H][d] bf16 out, contiguous, 16-byte aligned, or NULL
  *  lse   [total_q][H] fp32 out, contiguous, or NULL
@@ -472,7 +473,8 @@ kvc_status kvc_paged_append_workspace_size(const kvc_paged_cache* c, size_t* byt
  *             dropped); KVC_DEV_ERR_INDEX: an idx entry outside [0, len_b)
  *             (a zero row is written, at position -1 with weight 0)
  * The pages written must not be shared by two sequences of the batch, nor be
- * listed twice by one.  A sequence's new entries times Hkv: below 2^31.
+ * listed twice by one.  A sequence's new entries times Hkv: below 2^31; that
+ * times batch: below 2^38.  total = 0 with cu_seqlens: nothing is read or written.
  */
 kvc_status kvc_paged_append(const kvc_paged_cache* c, const uint16_t* k, const uint16_t* v, int64_t stride_n,
                             int64_t stride_h, const int32_t* cu_seqlens, int64_t total, int64_t max_seqlen,

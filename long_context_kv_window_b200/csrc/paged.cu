@@ -603,7 +603,10 @@ extern "C" kvc_status kvc_paged_append(const kvc_paged_cache* c, const uint16_t*
   a.err = dev_err;
   const int64_t most = (idx ? std::min(kk, max_seqlen) : max_seqlen) * a.c.Hkv;
   KVC_CHECK_ARG(most < (int64_t(1) << 31), "a sequence's new entries times num_kv_heads must be below 2^31");
-  const int64_t spans = std::max<int64_t>(1, (most + kAppSpan - 1) / kAppSpan);
+  // no sequence brings more than all tokens; the ticket counts the CTAs in 32 bits
+  const int64_t spans = std::max<int64_t>(1, (std::min(most, total * a.c.Hkv) + kAppSpan - 1) / kAppSpan);
+  KVC_CHECK_ARG(spans * a.c.batch < (int64_t(1) << 32),
+                "batch times a sequence's new entries times num_kv_heads must be below 2^38");
   const Launch l(dim3((unsigned)spans, (unsigned)a.c.batch), dim3(kAppThreads), 0, (cudaStream_t)stream);
   KVC_CUDA_TRY(a.c.d == 128 ? l.run(append_kernel<128>, a) : l.run(append_kernel<64>, a));
   count_launch();

@@ -278,3 +278,15 @@ def test_prefill_varlen_queries_where_the_bound_says_none():
                                          dev_err=err)
         torch.cuda.synchronize()
         assert err.item() == want and (out == 7).all() and (lse == 7).all()
+
+
+def test_append_with_a_bound_far_above_the_tokens():
+    rng = np.random.default_rng(19)
+    lens = [1, 0, 40]
+    t = Paged(rng, [5, 6, 7], 2, 64, 16, room=50)
+    k, kd = _bf16(rng, sum(lens), 2, 64)
+    kvc.kvc_paged_append(t.cache, kd, kd, _dev_i32(_cu(lens)), (1 << 30) - 1, dev_err=t.err)
+    ref.append(t.pool, k, k, _cu(lens))
+    t.check_state()
+    kvc.kvc_paged_append(t.cache, kd[:0], kd[:0], _dev_i32(_cu([0, 0, 0])), 9, dev_err=t.err)
+    t.check_state()

@@ -66,3 +66,21 @@ def test_prefill_workspace_is_that_of_the_tensors_device(monkeypatch):
         assert [kvc.prefill_varlen_workspace_size(*shape, torch.device("cuda", i)) for i in (0, 1, 0, 2)] == [
             1000, 1001, 1000, 1002]
     kvc._prefill_varlen_bytes.cache_clear()
+
+
+def test_append_beyond_the_counter_of_its_ctas_is_refused():
+    import ctypes
+
+    from long_context_kv_window_b200 import build
+    from tests.test_paged_checks import PTR, _cache
+    build.build()
+
+    def call(batch, total, most):
+        c = _cache(batch=batch, page_size=256, max_pages=1 << 22, table_stride=1 << 22, page_stride=1 << 15)
+        return kvc.lib().kvc_paged_append(ctypes.byref(c), PTR, PTR, 128, 64, PTR, total, most, None, 0, None, PTR, 256,
+                                          None, None)
+
+    before = kvc.launch_count()
+    assert call(1024, (1 << 31) - 1, (1 << 30) - 1) == 1 and "2^38" in kvc.last_error()
+    assert call(1024, 1 << 27, 1 << 28) == 1  # 2^28 entries of two heads, 1024 times
+    assert kvc.launch_count() == before
