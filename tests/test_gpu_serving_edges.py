@@ -290,3 +290,46 @@ def test_append_with_a_bound_far_above_the_tokens():
     t.check_state()
     kvc.kvc_paged_append(t.cache, kd[:0], kd[:0], _dev_i32(_cu([0, 0, 0])), 9, dev_err=t.err)
     t.check_state()
+
+
+def test_prefill_varlen_calls_that_overlap():
+    """Split and unsplit calls on two streams at once, eager and as two graphs
+    replayed at once: each as it is alone, to the last bit."""
+    rng = np.random.default_rng(23)
+    H, Hkv, d = 8, 2, 128
+    plans = [([900, 40, 2000, 3], [900, 40, 2000, 3]), ([16, 30], [5000, 4000])]
+    calls, want = [], []
+    for lq, lk in plans:
+        q, k, v = (_bf16(rng, n, h, d)[1] for n, h in ((sum(lq), H), (sum(lk), Hkv), (sum(lk), Hkv)))
+        cq, ck = _dev_i32(_cu(lq)), _dev_i32(_cu(lk))
+        out, lse = torch.empty_like(q), torch.empty((sum(lq), H), device="cuda")
+
+        def call(stream, q=q, k=k, v=v, cq=cq, ck=ck, lq=lq, lk=lk, out=out, lse=lse):
+            kvc.kvc_prefill_attention_varlen(q, k, v, cq, ck, max(lq), max(lk), out=out, lse=lse, stream=stream)
+            return out, lse
+        want.append([x.clone() for x in call(None)])
+        calls.append(call)
+    split = [kvc.prefill_varlen_workspace_size(H, Hkv, d, len(lq), sum(lq), max(lq), max(lk)) > 0 for lq, lk in plans]
+    assert split == [False, True]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    for call in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(None)
+    for replay in (False, True):
+        for call in calls:
+            for x in call(None):
+                x.zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for call, g, s in zip(calls, graphs, streams):
+                if replay:
+                    with torch.cuda.stream(s):
+                        g.replay()
+                else:
+                    call(s)
+        torch.cuda.synchronize()
+        for call, w in zip(calls, want):
+            out, lse = call.__defaults__[-2:]
+            assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
