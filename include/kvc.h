@@ -423,6 +423,11 @@ kvc_status kvc_prefill_attention_varlen(const uint16_t* q, int64_t q_stride_n, i
  * weights/pos[(p*num_kv_heads + g)*page_size + s % page_size].
  * All arrays are device memory of the caller; the struct itself is read
  * during the call only.
+ *
+ * Workspaces: the paged calls begin theirs with at most batch * num_kv_heads
+ * 32-bit counters, zero before and after every call.  One workspace (large
+ * enough for each) serves them all in turn, for caches of that many pairs or
+ * fewer; before its first use with a cache of more, zero-fill it again.
  */
 typedef struct kvc_paged_cache {
   uint16_t* k;                /* [num_pages][Hkv][page_size][d] bf16, 16-byte aligned */
@@ -506,7 +511,8 @@ kvc_status kvc_paged_decode_workspace_size(const kvc_paged_cache* c, int32_t num
  *  max_len  upper bound of seq_lens (host value), <= max_pages * page_size;
  *           the workspace of an accumulating call holds batch * num_heads *
  *           max_len floats, and the grid goes by it, so a bound near the
- *           longest sequence pays; batch * max_len below 2^36, batch * num_kv_heads * max_len below 2^40
+ *           longest sequence pays; batch * max_len below 2^36, batch *
+ *           num_kv_heads * max_len below 2^40
  *  out      [B][H][d] fp32, contiguous, 16-byte aligned
  *  lse      [B][H] fp32 contiguous, or NULL
  *  ws       kvc_paged_decode_workspace_size(...) bytes, 256-B aligned,

@@ -102,8 +102,9 @@ struct WsCursor {
 // never started while the kernel two places before it still runs.  Only
 // kernels whose grid is resident at once and whose dependents cannot hold
 // the SMs their own unscheduled CTAs would need trigger early (scoring pass 1,
-// the bias combine, the statistics); the others let their dependents launch
-// at completion.
+// the bias combine, the statistics, both decode attentions, eviction where its
+// CTAs are at most one per SM); the others let their dependents launch at
+// completion.
 struct Launch {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];

@@ -26,8 +26,10 @@ namespace {
 // within a head where a list selects them (the list and the pages then run
 // on).  Lengths move on once every CTA has read them: the last CTA of the grid (a ticket counter,
 // returned to zero) adds the new entries.  8 x 8 x 1024 selected rows (67 MB
-// in all) take 19.6 us cold, 3.4 TB/s: scattered reads of 256 bytes bound it.
-// One token for each of 64 sequences is four dependent round trips, 5 us.
+// in all) take 19.6 us cold, 3.4 TB/s in and out together (DRAM reads 1.9 TB/s
+// at 44 % of the warps).  What bounds it is the chain of lengths, list, rows and
+// stores that each of 1024 CTAs goes through once, four at a time on an SM: 1.7
+// waves with nothing of the next rows under way.  One token for each of 64 sequences is four dependent round trips, 5 us.
 constexpr int kAppThreads = 256;
 
 // A warp copies up to kRowItems items, lane i < kRowItems holding item i's
@@ -513,7 +515,8 @@ kvc_status check_evict(const Paged& c, int64_t max_len, int64_t budget) {
 
 // CTAs per pair: as many as the SMs hold at once (one of 1024 threads each),
 // with at least kEvSmall slots each.  32 pairs of 32768 entries cut to 2048,
-// what restores the cache between the calls included: 72.4 us with one CTA per
+// replayed from a graph, what restores the cache between the calls included
+// (called eagerly 60 to 63 us with four): 72.4 us with one CTA per
 // pair, 56.9 with two, 52.4 with four, 110.9 with eight (two waves).
 int evict_cluster(const Paged& c, int64_t max_len) {
   const int64_t pairs = (int64_t)c.batch * c.Hkv;

@@ -13,6 +13,8 @@
 // pairs; a pair that lies in one run is finished there, the others leave
 // (max, sum, output) per run and the last of their CTAs joins them in run
 // order (a ticket counter per pair, returned to zero).
+// A piece that met a page id outside the pool or an entry that did not arrive
+// has no result; nor has its pair, which adds no weights.
 //
 // Every warp streams its own 16 entries of each tile (one page holds them)
 // through a ring of its own -- TMA boxes, 128-byte swizzle, requested by the
@@ -22,8 +24,8 @@
 // the layout in which the second one takes P, so P stays in registers, which
 // the tcgen05 form cannot do; at 4 d bytes per entry the legacy tensor rate is
 // many times what the stream needs.  P enters as three bf16 terms, its 24 bits
-// (two, good to 2^-17, left the output 2.3e-6 off, three 5e-7, in the same
-// time); up to 8 heads per group the first two ride in one MMA, in rows 0..7
+// (two, good to 2^-17, left the output 2.3e-6 off, three 5e-7, for 1 to
+// 6 % of the time); up to 8 heads per group the first two ride in one MMA, in rows 0..7
 // and 8..15.  Row maxima are references that move only when a logit
 // passes them by more than 8 log2 units (a warp vote; p <= 2^8 otherwise).
 //

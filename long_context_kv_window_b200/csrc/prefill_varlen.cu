@@ -11,14 +11,19 @@
 // CTA holds two such tiles (2 * (128 / G) consecutive tokens) and walks the
 // key tiles of 128 up to its last row's limit:
 //   S_i = Q_i . K_t^T    M = 128 rows, N = 128 keys, K = d, fp32 in TMEM;
-//   P_i = 2^(S_i c - m)  one thread per row, c = scale * log2 e, m the row's
-//                        running reference; P_i goes back into TMEM as bf16
-//                        over S_i, the A operand of
+//   P_i = 2^(S_i c - m)  two threads per row, c = scale * log2 e, m the row's
+//                        reference; P_i goes back into TMEM as bf16 over S_i,
+//                        the A operand of
 //   O_i += P_i . V_t     M = 128, N = d, K = 128 keys, fp32 in TMEM.
 // The tensor core's shared-memory reads decide this layout: a 128^3 MMA with
 // both operands in shared memory reads 64 KB in the 512 cycles it computes,
 // all that an SM's shared memory delivers, so P in shared memory (written,
 // then read back) would bound the kernel at two thirds of the MMA rate.
+//
+// P enters as one bf16 term, as in the single-sequence call: at most 2^-8 of
+// itself off, so the output by at most 2^-8 of the mean of |v|, as much as its
+// own rounding to bf16.  A second term would be a third MMA per key tile.  The
+// sums and the log-sum-exp take the fp32 values.
 //
 // The reference m is the row's max over its first key tile.  bf16 has the range
 // of fp32 and its precision does not depend on the size of p, so m need not
@@ -45,13 +50,17 @@
 // Measured (32/8 heads, d = 128): 32K tokens 6.9 ms in bursts (1.27 PFLOP/s, 75 %
 // of the measured burst rate of a library GEMM), 7.8 to 7.9 ms for seconds on end
 // (1.12 PFLOP/s, 80 % of the sustained rate; the board's power bounds it: SM clock
-// 1.55 GHz); 8 prompts of 1K to 8K 1.55 ms; 512 prompts of 64 tokens 240 us.  A key tile takes 3400 cycles of 2048 that its MMAs need: per MMA
-// tile the softmax 1700 (1450 of them the exponentials, 1024 at the MUFU's rate)
-// and MMAs with their hand-overs 1700.  Tried: a part of the exponentials on the
+// 1.55 GHz); 8 prompts of 1K to 8K 1.55 to 1.64 ms; 512 prompts of 64 tokens 240 us.
+// A key tile takes 3400 cycles of 2048 that its MMAs need: per MMA tile the
+// softmax 1700 (1450 of them the exponentials, 1024 at the MUFU's rate) and MMAs
+// with their hand-overs 1700.  Tried: a part of the exponentials on the
 // FMA pipe as polynomials (1/8: 3 %, 1/2: 10 % slower: more instructions, more
 // power); 64-key logits in four chains (19 % slower: N = 64 MMAs take 450 cycles
 // where N = 128 ones take 512); half-signals of P; polling instead of suspended
 // waits (2 to 4 % slower).
+//
+// Few rows over many keys: the keys of a block are shared among CTAs, whose
+// (log-sum-exp, output) a second kernel joins.
 //
 // Keys a row does not see are masked before the max.  A masked value row still
 // meets p = 0 in the MMA, and 0 * inf = NaN; so the value tiles in which some
@@ -275,7 +284,8 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   // The block of CTA `item` of the grid, by a warp: the splits of a block side by
   // side, then its heads, then the blocks, the last (longest) of a sequence
   // first; up to 32 sequences the longest first, more in order.  Four chunks of
-  // 512 queries over 8K to 32K keys: 1010 us in order, 836 us sorted.
+  // 512 queries over 8K to 32K keys: 1010 us in order, 836 us sorted (in turn, at
+  // that step; 850 to 890 us since).
   // It looks at 32 sequences, one per lane, and keeps them for the next search.
   int cur_b = 0, cur_before = 0, cur_blocks = 0;  // the first of them, blocks before it, their blocks
   int c_nb = 0, c_before = 0, c_q0 = 0, c_k0 = 0, c_lq = 0, c_lk = 0;  // the lane's: blocks, blocks of them before it
@@ -435,8 +445,11 @@ prefill_varlen_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       }
     } else if (warp < 3) {
       // ---- MMA issuers, one per MMA tile: S of key tile 0, then for every key
-      // tile the output and the next logits (which overwrite the P just used:
-      // the tensor core runs a thread's MMAs in the order they are issued).
+      // tile the output and the next logits, which overwrite the P just used with
+      // no wait between the two.  That relies on the tensor core running the MMAs
+      // of one issuing thread one after another, in order: PTX promises the order
+      // only for MMAs of the same accumulator and shape, which these are not; what
+      // is known of it here is that no comparison, of any length, showed otherwise.
       // The tensor core queues hardly ahead, so what a warp spends on waits and
       // commits would leave it idle; the other tile's MMAs fill that.  They
       // take turns, the next one invited two MMAs early: mixed, both tiles'
