@@ -426,8 +426,9 @@ kvc_status kvc_prefill_attention_varlen(const uint16_t* q, int64_t q_stride_n, i
  *
  * Workspaces: the paged calls begin theirs with at most batch * num_kv_heads
  * 32-bit counters, zero before and after every call.  One workspace (large
- * enough for each) serves them all in turn, for caches of that many pairs or
- * fewer; before its first use with a cache of more, zero-fill it again.
+ * enough for each) serves them all in turn.  What follows a cache's counters
+ * is not kept zero: before a workspace goes to a cache of more pairs than the
+ * one before, zero-fill it again.
  */
 typedef struct kvc_paged_cache {
   uint16_t* k;                /* [num_pages][Hkv][page_size][d] bf16, 16-byte aligned */

@@ -600,7 +600,9 @@ def prefill_varlen_workspace_size(H: int, Hkv: int, d: int, batch: int, total_q:
                                   dev: Optional[torch.device] = None) -> int:
     """Workspace bytes of a call with these sizes on `dev`, whose number of SMs
     they depend on (default: the current device)."""
-    index = dev.index if dev is not None else torch.cuda.current_device() if torch.cuda.is_available() else None
+    index = None if dev is None else dev.index
+    if index is None and torch.cuda.is_available():
+        index = torch.cuda.current_device()
     return _prefill_varlen_bytes(index, H, Hkv, d, batch, total_q, max_q, max_k)
 
 
